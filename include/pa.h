@@ -71,7 +71,8 @@ enum {
     PA_DEVERR_TABLE = 2,        /* a table entry outside [0, num_blocks) */
     PA_DEVERR_TIMEOUT = 4,      /* a pipeline wait gave up (the kernel returned early) */
     PA_DEVERR_CACHE_LEN = 8,    /* append: cache_len < 0 or >= max_blocks*bs */
-    PA_DEVERR_COPY = 16         /* block copy: an id outside [0, num_blocks) */
+    PA_DEVERR_COPY = 16,        /* block copy: an id outside [0, num_blocks) */
+    PA_DEVERR_NO_BLOCKS = 32    /* step maps: the free list has too few blocks */
 };
 
 /* Kernel selection for pa_decode (pa_plan_set_path). */
@@ -499,6 +500,150 @@ pa_status pa_decode_noalloc(const void* q, const void* k_pool, const void* v_poo
                             int B, int Hq, int Hkv, int D, int block_size, int num_blocks,
                             int max_seq_len, float scale, pa_dtype kv_dtype, void* out,
                             pa_dtype out_dtype, int* device_error, struct CUstream_st* stream);
+
+/* ------------------------------------------------------------------------
+ * A serving step's preparation: block tables and slots, the rotation of
+ * queries and keys, and the cache write of any number of rows.
+ * ---------------------------------------------------------------------- */
+
+/*
+ * pa_step_maps -- the block tables, lengths and slots of a step, on the device.
+ *
+ * Request b has cache_lens[b] cached tokens and adds new_lens[b] >= 0 (a
+ * decode step 1, a prompt chunk many, an idle request 0). Its tokens fill
+ * blocks in order and any free block fits ("PagedAttention: The Cache Was
+ * Storing Nothing" §2.2). The call writes
+ *   seq_lens[b]   cache_lens[b] + new_lens[b]
+ *   q_start[b]    rows of the requests before b; q_start[B] = all rows
+ *   block_tables  entries ceil(cache_b / bs) .. ceil(seq_b / bs) - 1 of row b
+ *                 (fresh blocks); the others keep their values
+ *   positions[t]  row t's position in its request, cache_lens[b] + t - q_start[b]
+ *   slots[t]      block * block_size + offset of that position in the pools
+ *   free_left[0]  free_count[0] less the blocks taken
+ * for seq_lens and q_start as pa_decode, pa_decode_multi, pa_prefill and their
+ * windowed forms take them, positions and slots as pa_qk_rope_append does.
+ * Rows t >= q_start[B] (a batch padded to num_rows) get position 0, slot -1.
+ *
+ *   cache_lens, new_lens  device int32 [B], read only; B <= 8192
+ *   free_blocks   device int32 [num_free]: a stack of free block ids (e.g.
+ *                 from pa_bm_alloc); the first fresh block of the first
+ *                 request that needs one is free_blocks[free_count[0] - 1],
+ *                 the next the entry below it, request by request. Read only
+ *   free_count    device int32 [1], read only, 0 .. num_free
+ *   num_rows      host: rows of positions and slots, >= the sum of new_lens
+ *   device_error  device int or NULL (the library-wide word): PA_DEVERR_* bits
+ *
+ * A written block must be private to its request: a shared, partly filled
+ * last block is copied first (pa_bm_prepare_append, pa_copy_blocks). All or
+ * nothing: when the free list is too short, no block is taken, every request
+ * that needs one gets seq_lens 0 and slots -1, and PA_DEVERR_NO_BLOCKS is
+ * raised; requests that need none are served. A negative length, a length
+ * over min(max_seq_len, max_blocks * block_size) or rows past num_rows raise
+ * PA_DEVERR_SEQ_LEN and give that request seq_lens 0 and slots -1 (a negative
+ * new_lens counts as no rows, q_start stays within num_rows). A table entry or
+ * free block outside [0, num_blocks), or a free_count outside [0, num_free]
+ * (taken as 0), raises PA_DEVERR_TABLE; the slots it concerns are -1, the
+ * table entry is written as it is and later calls refuse it. seq_lens and
+ * q_start must not overlap cache_lens or new_lens, nor free_left free_count
+ * (PA_ERR_SHAPE): chained steps alternate between two buffers. B = 0 is a
+ * no-op. One launch; results do not depend on timing.
+ */
+pa_status pa_step_maps(const int32_t* cache_lens, const int32_t* new_lens, int B,
+                       const int32_t* free_blocks, int num_free, const int32_t* free_count,
+                       int32_t* block_tables, int max_blocks, int block_size, int num_blocks,
+                       int max_seq_len, int32_t* seq_lens, int32_t* q_start, int32_t* positions,
+                       int64_t* slots, int num_rows, int32_t* free_left, int* device_error,
+                       struct CUstream_st* stream);
+
+/* Which elements of a head make a rotated pair i < rot_dim / 2. */
+enum {
+    PA_ROPE_HALF = 0,        /* (i, i + rot_dim / 2) */
+    PA_ROPE_INTERLEAVED = 1  /* (2i, 2i + 1) */
+};
+
+/* How pa_rope_inv_freq scales the frequencies f_i = base^(-2i / rot_dim). */
+enum {
+    PA_ROPE_NONE = 0,
+    PA_ROPE_LINEAR = 1, /* f_i / factor: positions interpolated */
+    PA_ROPE_PARTS = 2,  /* kept above high_turns turns over orig_len, f_i / factor below
+                           low_turns, a linear ramp in the turns between ("NTK by parts",
+                           YaRN paper, arXiv 2309.00071, section 3.2) */
+    PA_ROPE_YARN = 3    /* the same ends, with the ramp linear in i between the rounded pair
+                           indices, and amplitude 0.1 ln(factor) + 1 (section 3.3) */
+};
+
+#define PA_ROPE_MAX_PAIRS 64
+
+/* A rotation, in host memory, filled by pa_rope_init and read by each call
+ * (nothing refers to it afterwards). */
+typedef struct {
+    int32_t rot_dim;   /* rotated elements: the first rot_dim of a head */
+    int32_t layout;    /* PA_ROPE_HALF or PA_ROPE_INTERLEAVED */
+    float amplitude;   /* factor on the rotated elements */
+    int32_t reserved;
+    uint64_t turn[PA_ROPE_MAX_PAIRS]; /* 2^64 x the part of a turn that pair i makes a position */
+} pa_rope;
+
+/* Frequencies (radians a position) of the rot_dim / 2 pairs into inv_freq and
+ * the matching amplitude. rot_dim: a multiple of 16 up to 128; base > 1;
+ * factor >= 1; 0 < low_turns < high_turns (1 and 32 in the YaRN paper, 1 and 4
+ * for models trained so). Arguments a scaling does not name are not read. */
+pa_status pa_rope_inv_freq(int rot_dim, double base, int scaling, double factor, double orig_len,
+                           double low_turns, double high_turns, double* inv_freq,
+                           float* amplitude);
+/* A rotation from any frequencies (finite, radians a position). */
+pa_status pa_rope_init(pa_rope* rope, int rot_dim, int layout, const double* inv_freq,
+                       float amplitude);
+
+/*
+ * pa_qk_rope -- norm and rotate the queries and keys of num_rows rows.
+ *
+ * Row t of q ([Hq][D]) and k ([Hk][D]) starts t * stride elements after the
+ * first (the heads of a row are contiguous), so both may be views of a fused
+ * projection. Per head: with a weight, x <- x * w / sqrt(mean(x^2) + eps);
+ * then, over the first rope->rot_dim elements, pair i turns by the angle
+ * positions[t] * inv_freq[i] and is scaled by the amplitude. Computed in 32
+ * bits and rounded once; elements neither normed nor rotated keep their bits.
+ *
+ *   positions  device int32 [num_rows], any value (negative ones turn back)
+ *   q_weight, k_weight  device [D] of dtype, or NULL: no norm of q / of k
+ *   eps        >= 0, finite
+ *   rope       host, or NULL: no rotation; rot_dim <= D
+ *   q_out, k_out  rows as q and k, of dtype; each may be its own input (same
+ *              pointer and stride) and must not overlap anything else
+ *
+ * dtype PA_BF16 or PA_F32, D 64 or 128. Strides: at least a row, whole 16-byte
+ * units; pointers 16-byte aligned. num_rows = 0 is a no-op.
+ */
+pa_status pa_qk_rope(const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                     const int32_t* positions, int num_rows, int Hq, int Hk, int D, pa_dtype dtype,
+                     const void* q_weight, const void* k_weight, float eps, const pa_rope* rope,
+                     void* q_out, int64_t q_out_stride, void* k_out, int64_t k_out_stride,
+                     struct CUstream_st* stream);
+
+/*
+ * pa_qk_rope_append -- pa_qk_rope, with the keys and the values written to the
+ * paged pools: the step's cache write for any number of rows per request.
+ *
+ * Row t's keys (normed, rotated) and values (bit for bit) go to slot slots[t]
+ * = block * block_size + offset of k_pool and v_pool ([num_blocks][Hkv]
+ * [block_size][D]); the queries go to q_out as in pa_qk_rope.
+ *
+ *   slots  device int64 [num_rows] (pa_step_maps): distinct, or -1: a padding
+ *          row, for which nothing is read or written. Any other value outside
+ *          [0, num_blocks * block_size) skips the row and raises
+ *          PA_DEVERR_TABLE in device_error (device int, or NULL: the
+ *          library-wide word)
+ *
+ * Written blocks must be private to their request, as for pa_append_kv.
+ */
+pa_status pa_qk_rope_append(const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                            const void* v, int64_t v_stride, const int32_t* positions,
+                            const int64_t* slots, int num_rows, int Hq, int Hkv, int D,
+                            pa_dtype dtype, const void* q_weight, const void* k_weight, float eps,
+                            const pa_rope* rope, void* q_out, int64_t q_out_stride, void* k_pool,
+                            void* v_pool, int block_size, int num_blocks, int* device_error,
+                            struct CUstream_st* stream);
 
 #ifdef __cplusplus
 }

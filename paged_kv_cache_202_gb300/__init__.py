@@ -30,10 +30,13 @@ PA_OK, PA_ERR_NULL, PA_ERR_SHAPE, PA_ERR_DTYPE, PA_ERR_BLOCK_SIZE = 0, 1, 2, 3, 
 PA_ERR_WORKSPACE, PA_ERR_CUDA, PA_ERR_BOUNDS, PA_ERR_ALIGN, PA_ERR_NO_BLOCKS = 5, 6, 7, 8, 9
 PA_F32, PA_BF16 = 0, 1
 PA_DEVERR_SEQ_LEN, PA_DEVERR_TABLE, PA_DEVERR_TIMEOUT, PA_DEVERR_CACHE_LEN = 1, 2, 4, 8
-PA_DEVERR_COPY = 16
+PA_DEVERR_COPY, PA_DEVERR_NO_BLOCKS = 16, 32
 PA_PATH_AUTO, PA_PATH_SIMPLE, PA_PATH_FMA, PA_PATH_MMA, PA_PATH_PREFILL = 0, 1, 2, 3, 4
 PA_MERGE_AUTO, PA_MERGE_KERNEL, PA_MERGE_FUSED = 0, 1, 2
 PA_SIMPLE_MAX_SEQ_LEN = 8192   # longest max_seq_len of the unsplit kernel (float32 pools)
+PA_ROPE_HALF, PA_ROPE_INTERLEAVED = 0, 1
+PA_ROPE_NONE, PA_ROPE_LINEAR, PA_ROPE_PARTS, PA_ROPE_YARN = 0, 1, 2, 3
+PA_ROPE_MAX_PAIRS = 64
 
 _lib = None
 
@@ -105,6 +108,22 @@ def lib() -> ctypes.CDLL:
     L.pa_decode_multi.restype = ci
     L.pa_page_scores.argtypes = [vp, vp, vp, ci, vp, ci, ci, ci, ci, ci, ci, ci, vp, vp, vp, vp]
     L.pa_page_scores.restype = ci
+    i64 = ctypes.c_int64
+    f64p = ctypes.POINTER(ctypes.c_double)
+    L.pa_step_maps.argtypes = [vp, vp, ci, vp, ci, vp, vp, ci, ci, ci, ci, vp, vp, vp, vp, ci, vp,
+                               vp, vp]
+    L.pa_step_maps.restype = ci
+    L.pa_rope_inv_freq.argtypes = [ci, ctypes.c_double, ci, ctypes.c_double, ctypes.c_double,
+                                   ctypes.c_double, ctypes.c_double, f64p, ctypes.POINTER(cf)]
+    L.pa_rope_inv_freq.restype = ci
+    L.pa_rope_init.argtypes = [vp, ci, ci, f64p, cf]
+    L.pa_rope_init.restype = ci
+    L.pa_qk_rope.argtypes = [vp, i64, vp, i64, vp, ci, ci, ci, ci, ci, vp, vp, cf, vp, vp, i64, vp,
+                             i64, vp]
+    L.pa_qk_rope.restype = ci
+    L.pa_qk_rope_append.argtypes = [vp, i64, vp, i64, vp, i64, vp, vp, ci, ci, ci, ci, ci, vp, vp,
+                                    cf, vp, vp, i64, vp, vp, ci, ci, vp, vp]
+    L.pa_qk_rope_append.restype = ci
     for name in ("pa_bm_create", "pa_bm_destroy", "pa_bm_alloc", "pa_bm_fork", "pa_bm_release",
                  "pa_bm_refcount", "pa_bm_num_free", "pa_bm_prepare_append"):
         getattr(L, name).restype = ci
@@ -391,6 +410,188 @@ def pa_page_scores(k_pool: torch.Tensor, v_pool: torch.Tensor, block_tables: tor
                               B, Hkv, D, bs, NB, int(max_seq_len), _dtype(k_pool), _ptr(scores),
                               _ptr(victims), err, _stream(stream))
     _check(st, "pa_page_scores")
+
+
+# ------------------------------------------------------------------ step preparation
+
+class _RopeStruct(ctypes.Structure):
+    _fields_ = [("rot_dim", ctypes.c_int32), ("layout", ctypes.c_int32),
+                ("amplitude", ctypes.c_float), ("reserved", ctypes.c_int32),
+                ("turn", ctypes.c_uint64 * PA_ROPE_MAX_PAIRS)]
+
+
+class Rope:
+    """A rotation (``pa_rope``): the first ``rot_dim`` elements of a head in the
+    given pair layout, with frequencies ``base^(-2i / rot_dim)`` scaled as
+    ``scaling`` says (``pa_rope_inv_freq``), or with ``inv_freq`` (radians a
+    position, one value per pair) as they are. ``amplitude`` replaces the
+    factor that belongs to the scaling."""
+
+    def __init__(self, rot_dim: int, layout: int = PA_ROPE_HALF, base: float = 10000.0,
+                 scaling: int = PA_ROPE_NONE, factor: float = 1.0, orig_len: float = 0.0,
+                 low_turns: float = 1.0, high_turns: float = 32.0, inv_freq=None,
+                 amplitude: float | None = None):
+        freq = (ctypes.c_double * PA_ROPE_MAX_PAIRS)()
+        amp = ctypes.c_float(1.0)
+        if inv_freq is None:
+            _check(lib().pa_rope_inv_freq(int(rot_dim), float(base), int(scaling), float(factor),
+                                          float(orig_len), float(low_turns), float(high_turns),
+                                          freq, ctypes.byref(amp)), "pa_rope_inv_freq")
+        else:
+            if len(inv_freq) != rot_dim // 2 or len(inv_freq) > PA_ROPE_MAX_PAIRS:
+                raise ValueError(f"inv_freq has {len(inv_freq)} values, expected {rot_dim // 2}")
+            freq[:len(inv_freq)] = [float(x) for x in inv_freq]
+        if amplitude is not None:
+            amp.value = float(amplitude)
+        self.struct = _RopeStruct()
+        _check(lib().pa_rope_init(ctypes.byref(self.struct), int(rot_dim), int(layout), freq, amp),
+               "pa_rope_init")
+        self.inv_freq = list(freq[:rot_dim // 2])
+        self.amplitude = amp.value
+        self.address = ctypes.addressof(self.struct)   # what the calls pass; the struct stays with self
+
+
+def _one_device(what: str, ts) -> torch.device:
+    """The CUDA device that all given tensors are on."""
+    dev = ts[0].device
+    for t in ts:
+        if t.device != dev:
+            raise ValueError(f"{what}: tensors on {dev} and {t.device}: all must be on one device")
+    if dev.type != "cuda":
+        raise ValueError(f"{what}: tensors must be on a CUDA device")
+    return dev
+
+
+def _call(what: str, fn, dev: torch.device, stream, *args) -> None:
+    """Call fn(*args, stream) with dev current, on its current stream by default."""
+    if stream is None:
+        stream = torch.cuda.current_stream(dev).cuda_stream
+    elif hasattr(stream, "cuda_stream"):
+        stream = stream.cuda_stream
+    if dev.index == torch.cuda.current_device():
+        st = fn(*args, stream)
+    else:
+        with torch.cuda.device(dev):
+            st = fn(*args, stream)
+    if st != PA_OK:
+        raise PagedAttentionError(st, what)
+
+
+def _rows(t: torch.Tensor, name: str, shape: tuple, dtype: torch.dtype) -> tuple[int, int]:
+    """(address, row stride) of [rows, H, D] rows whose heads are contiguous."""
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {shape}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} is {t.dtype}, expected {dtype}")
+    T, H, D = shape
+    s0, s1, s2 = t.stride()
+    if s2 != 1 or (H > 1 and s1 != D):
+        raise ValueError(f"{name}: the heads of a row must be contiguous")
+    return t.data_ptr(), (s0 if T > 1 else H * D)
+
+
+def _vector(t: torch.Tensor, name: str, n: int, dtype: torch.dtype) -> int:
+    if t.dtype != dtype:
+        raise TypeError(f"{name} is {t.dtype}, expected {dtype}")
+    if t.dim() != 1 or t.shape[0] != n:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected ({n},)")
+    if n > 1 and t.stride(0) != 1:
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def pa_step_maps(cache_lens: torch.Tensor, new_lens: torch.Tensor, free_blocks: torch.Tensor,
+                 free_count: torch.Tensor, block_tables: torch.Tensor, block_size: int,
+                 num_blocks: int, max_seq_len: int, seq_lens: torch.Tensor, q_start: torch.Tensor,
+                 positions: torch.Tensor, slots: torch.Tensor, free_left: torch.Tensor,
+                 device_error: torch.Tensor | None = None, stream=None) -> None:
+    """Build a step's maps on the device from the requests' lengths: fresh blocks
+    into ``block_tables`` (in place), ``seq_lens`` [B], ``q_start`` [B + 1],
+    ``positions`` (int32) and ``slots`` (int64) of every row, ``free_left`` [1].
+
+    ``free_blocks`` is a stack of free block ids of which ``free_count`` [1]
+    are valid; ``slots`` may have more rows than the step (padding: slot -1).
+    """
+    i32 = torch.int32
+    B, T = cache_lens.shape[0], slots.shape[0]
+    ts = [cache_lens, new_lens, free_blocks, free_count, block_tables, seq_lens, q_start, positions,
+          slots, free_left]
+    if device_error is not None:
+        ts.append(device_error)
+    dev = _one_device("pa_step_maps", ts)
+    _expect(block_tables, "block_tables", (B, block_tables.shape[-1]), i32)
+    _call("pa_step_maps", lib().pa_step_maps, dev, stream,
+          _vector(cache_lens, "cache_lens", B, i32), _vector(new_lens, "new_lens", B, i32), B,
+          _vector(free_blocks, "free_blocks", free_blocks.shape[0], i32) or free_count.data_ptr(),
+          free_blocks.shape[0], _vector(free_count, "free_count", 1, i32), _ptr(block_tables),
+          block_tables.shape[1], int(block_size), int(num_blocks), int(max_seq_len),
+          _vector(seq_lens, "seq_lens", B, i32), _vector(q_start, "q_start", B + 1, i32),
+          _vector(positions, "positions", T, i32), _vector(slots, "slots", T, torch.int64), T,
+          _vector(free_left, "free_left", 1, i32), _error_word(device_error))
+
+
+def pa_qk_rope(q: torch.Tensor, k: torch.Tensor, positions: torch.Tensor, rope: Rope | None,
+               q_out: torch.Tensor, k_out: torch.Tensor, q_weight: torch.Tensor | None = None,
+               k_weight: torch.Tensor | None = None, eps: float = 1e-6, stream=None) -> None:
+    """Norm (where a weight is given) and rotate ``q`` [T, Hq, D] and ``k`` [T, Hk, D]
+    into ``q_out`` and ``k_out``, which may be the inputs themselves. Rows may
+    be strided (views of a fused projection); the heads of a row are contiguous."""
+    T, Hq, D = q.shape
+    Hk = k.shape[1]
+    dt = q.dtype
+    ts = [q, k, positions, q_out, k_out]
+    qw = kw = None
+    if q_weight is not None:
+        ts.append(q_weight)
+        qw = _vector(q_weight, "q_weight", D, dt)
+    if k_weight is not None:
+        ts.append(k_weight)
+        kw = _vector(k_weight, "k_weight", D, dt)
+    dev = _one_device("pa_qk_rope", ts)
+    qp, qs = _rows(q, "q", (T, Hq, D), dt)
+    kp, ks = _rows(k, "k", (T, Hk, D), dt)
+    qo, qos = _rows(q_out, "q_out", (T, Hq, D), dt)
+    ko, kos = _rows(k_out, "k_out", (T, Hk, D), dt)
+    if T == 0:
+        return
+    _call("pa_qk_rope", lib().pa_qk_rope, dev, stream, qp, qs, kp, ks,
+          _vector(positions, "positions", T, torch.int32), T, Hq, Hk, D, _dtype(q), qw, kw,
+          float(eps), rope.address if rope is not None else None, qo, qos, ko, kos)
+
+
+def pa_qk_rope_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, positions: torch.Tensor,
+                      slots: torch.Tensor, rope: Rope | None, k_pool: torch.Tensor,
+                      v_pool: torch.Tensor, q_out: torch.Tensor,
+                      q_weight: torch.Tensor | None = None, k_weight: torch.Tensor | None = None,
+                      eps: float = 1e-6, device_error: torch.Tensor | None = None,
+                      stream=None) -> None:
+    """``pa_qk_rope`` with the keys and values written to the paged pools at
+    ``slots`` (int64 [T]; -1 marks a padding row, which is left alone)."""
+    T, Hq, D = q.shape
+    NB, Hkv, bs, _ = _pools(k_pool, v_pool)
+    dt = q.dtype
+    ts = [q, k, v, positions, slots, k_pool, v_pool, q_out]
+    qw = kw = None
+    if q_weight is not None:
+        ts.append(q_weight)
+        qw = _vector(q_weight, "q_weight", D, dt)
+    if k_weight is not None:
+        ts.append(k_weight)
+        kw = _vector(k_weight, "k_weight", D, dt)
+    if device_error is not None:
+        ts.append(device_error)
+    dev = _one_device("pa_qk_rope_append", ts)
+    _expect(k_pool, "k_pool", (NB, Hkv, bs, D), dt)
+    qp, qs = _rows(q, "q", (T, Hq, D), dt)
+    kp, ks = _rows(k, "k", (T, Hkv, D), dt)
+    vp, vs = _rows(v, "v", (T, Hkv, D), dt)
+    qo, qos = _rows(q_out, "q_out", (T, Hq, D), dt)
+    if T == 0:
+        return
+    _call("pa_qk_rope_append", lib().pa_qk_rope_append, dev, stream, qp, qs, kp, ks, vp, vs,
+          _vector(positions, "positions", T, torch.int32), _vector(slots, "slots", T, torch.int64),
+          T, Hq, Hkv, D, _dtype(q), qw, kw, float(eps), rope.address if rope is not None else None,
+          qo, qos, _ptr(k_pool), _ptr(v_pool), bs, NB, _error_word(device_error))
 
 
 class BlockManager:

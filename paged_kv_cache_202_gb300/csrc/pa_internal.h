@@ -24,6 +24,7 @@ constexpr int kErrTable = 2;
 constexpr int kErrTimeout = 4;
 constexpr int kErrCacheLen = 8;
 constexpr int kErrCopy = 16;
+constexpr int kErrNoBlocks = 32;
 
 // Wall-clock limit of any single pipeline wait inside a kernel.
 constexpr uint64_t kWaitLimitNs = 2000000000ull;  // 2 s
