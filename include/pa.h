@@ -645,6 +645,68 @@ pa_status pa_qk_rope_append(const void* q, int64_t q_stride, const void* k, int6
                             void* v_pool, int block_size, int num_blocks, int* device_error,
                             struct CUstream_st* stream);
 
+/*
+ * pa_decode_window -- pa_decode with a sliding window and sinks.
+ *
+ * The new query of sequence b, at position L_b - 1, attends to the tokens
+ * t >= L_b - window (the window holds the token itself) and to the sequence's
+ * first `sinks` tokens, which stay visible:
+ *   out[b][h][:] = sum_t w_t v_t,  w = softmax_t(scale * q[b][h] . k_t) over
+ *   t < L_b with L_b - t <= window or t < sinks.
+ * Only pages that hold such a token are read: table entries of the pages
+ * between the sinks and the window are never looked at and may name blocks
+ * that were given back, and keys and values of hidden tokens in the pages at
+ * either end never reach a result, whatever they hold.
+ *
+ *   window    >= 1;  sinks >= 0 (0: a plain sliding window)
+ *   other arguments, limits and device errors as for pa_decode, bf16 pools only
+ *   (PA_ERR_DTYPE); the plan's forced path does not apply, PA_MERGE_FUSED is
+ *   refused (PA_ERR_SHAPE). seq_lens are the full lengths.
+ *
+ * Cost: the bytes of min(L_b, window + sinks) tokens rounded to pages. Calls
+ * on one plan must be ordered on the device (one stream, or events): they
+ * share its workspace. A call that needs a larger workspace during a stream
+ * capture returns PA_ERR_WORKSPACE: make the call once before capturing it.
+ * Memory that this call and pa_prefill_window outgrow is kept until pa_free,
+ * so graphs captured with the plan stay valid.
+ */
+pa_status pa_decode_window(const void* q, const void* k_pool, const void* v_pool,
+                           const int32_t* block_tables, int max_blocks, const int32_t* seq_lens,
+                           int B, int Hq, int Hkv, int D, int block_size, int num_blocks,
+                           int max_seq_len, float scale, int window, int sinks, pa_dtype kv_dtype,
+                           void* out, pa_dtype out_dtype, pa_plan** plan_inout,
+                           struct CUstream_st* stream);
+
+/*
+ * pa_prefill_window -- the same for the newest queries of every sequence:
+ * prompts, prompt chunks and the verification of drafted tokens.
+ *
+ * Query i of the n_b = q_start[b+1] - q_start[b] queries of sequence b, at
+ * position p = L_b - n_b + i, attends to the tokens t <= p with p - t < window
+ * or t < sinks; the K/V of the new tokens are already in the pools. Pages that
+ * hold no token visible to a tile of 128 / (Hq / Hkv) queries (two tiles in
+ * large calls) are not read for it, so blocks behind the first query's window
+ * may have been given back. Values of tokens that some queries of a tile see
+ * and others do not must be finite.
+ *
+ *   q, q_start, num_queries, max_q, out   as for pa_prefill; n_b = 0 is allowed
+ *   window, sinks, plan_inout             as for pa_decode_window
+ *   scale                                 > 0
+ *
+ * bf16 pools, D = 128, Hq / Hkv dividing 128, max_blocks <= 16384, B <= 8192
+ * and Hkv <= 65535 (PA_ERR_DTYPE / PA_ERR_SHAPE otherwise). Few tiles split
+ * their key range over blocks as in pa_decode_multi. An invalid sequence gets
+ * zero rows and PA_DEVERR_SEQ_LEN, a table entry outside the pool zeroes the
+ * rows it concerns and raises PA_DEVERR_TABLE, both in the plan's error word.
+ * q_start must be nondecreasing. num_queries = 0 or B = 0 is a no-op.
+ */
+pa_status pa_prefill_window(const void* q, const int32_t* q_start, int num_queries, int max_q,
+                            const void* k_pool, const void* v_pool, const int32_t* block_tables,
+                            int max_blocks, const int32_t* seq_lens, int B, int Hq, int Hkv, int D,
+                            int block_size, int num_blocks, int max_seq_len, float scale,
+                            int window, int sinks, pa_dtype kv_dtype, void* out,
+                            pa_dtype out_dtype, pa_plan** plan_inout, struct CUstream_st* stream);
+
 #ifdef __cplusplus
 }
 #endif

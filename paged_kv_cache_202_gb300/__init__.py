@@ -124,6 +124,12 @@ def lib() -> ctypes.CDLL:
     L.pa_qk_rope_append.argtypes = [vp, i64, vp, i64, vp, i64, vp, vp, ci, ci, ci, ci, ci, vp, vp,
                                     cf, vp, vp, i64, vp, vp, ci, ci, vp, vp]
     L.pa_qk_rope_append.restype = ci
+    L.pa_decode_window.argtypes = [vp, vp, vp, vp, ci, vp, ci, ci, ci, ci, ci, ci, ci, cf, ci, ci,
+                                   ci, vp, ci, ctypes.POINTER(vp), vp]
+    L.pa_decode_window.restype = ci
+    L.pa_prefill_window.argtypes = [vp, vp, ci, ci, vp, vp, vp, ci, vp, ci, ci, ci, ci, ci, ci, ci,
+                                    cf, ci, ci, ci, vp, ci, ctypes.POINTER(vp), vp]
+    L.pa_prefill_window.restype = ci
     for name in ("pa_bm_create", "pa_bm_destroy", "pa_bm_alloc", "pa_bm_fork", "pa_bm_release",
                  "pa_bm_refcount", "pa_bm_num_free", "pa_bm_prepare_append"):
         getattr(L, name).restype = ci
@@ -592,6 +598,56 @@ def pa_qk_rope_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, positio
           _vector(positions, "positions", T, torch.int32), _vector(slots, "slots", T, torch.int64),
           T, Hq, Hkv, D, _dtype(q), qw, kw, float(eps), rope.address if rope is not None else None,
           qo, qos, _ptr(k_pool), _ptr(v_pool), bs, NB, _error_word(device_error))
+
+
+def _check_window(what, q, k_pool, v_pool, block_tables, seq_lens, out, B: int, *more) -> tuple:
+    dev = _one_device(what, (q, k_pool, v_pool, block_tables, seq_lens, out, *more))
+    if q.dtype != k_pool.dtype:
+        raise TypeError(f"q is {q.dtype}, the pools are {k_pool.dtype}")
+    if q.shape[2] != k_pool.shape[3]:
+        raise ValueError(f"q has {q.shape[2]} elements a head, the pools {k_pool.shape[3]}")
+    _expect(out, "out", tuple(q.shape))
+    _expect(block_tables, "block_tables", (B, block_tables.shape[-1]), torch.int32)
+    _expect(seq_lens, "seq_lens", (B,), torch.int32)
+    return dev
+
+
+def pa_decode_window(q: torch.Tensor, k_pool: torch.Tensor, v_pool: torch.Tensor,
+                     block_tables: torch.Tensor, seq_lens: torch.Tensor, scale: float, window: int,
+                     sinks: int, out: torch.Tensor, max_seq_len: int, plan: Plan,
+                     stream=None) -> torch.Tensor:
+    """Paged decode attention over the last ``window`` tokens and the first
+    ``sinks`` tokens of every sequence into ``out``; returns ``out`` (bf16 pools).
+    Table entries of pages between the two are never read."""
+    B, Hq, D = q.shape
+    NB, Hkv, bs, _ = _pools(k_pool, v_pool)
+    dev = _check_window("pa_decode_window", q, k_pool, v_pool, block_tables, seq_lens, out, B)
+    _call("pa_decode_window", lib().pa_decode_window, dev, stream, _ptr(q), _ptr(k_pool),
+          _ptr(v_pool), _ptr(block_tables), block_tables.shape[1], _ptr(seq_lens), B, Hq, Hkv, D,
+          bs, NB, int(max_seq_len), float(scale), int(window), int(sinks), _dtype(k_pool),
+          _ptr(out), _dtype(out), ctypes.byref(plan.handle))
+    return out
+
+
+def pa_prefill_window(q: torch.Tensor, q_start: torch.Tensor, k_pool: torch.Tensor,
+                      v_pool: torch.Tensor, block_tables: torch.Tensor, seq_lens: torch.Tensor,
+                      scale: float, window: int, sinks: int, out: torch.Tensor, max_q: int,
+                      max_seq_len: int, plan: Plan, stream=None) -> torch.Tensor:
+    """``pa_decode_window`` for the newest queries of every sequence (rows as for
+    ``pa_prefill``; bf16 pools, D = 128); returns ``out``."""
+    T, Hq, D = q.shape
+    NB, Hkv, bs, _ = _pools(k_pool, v_pool)
+    B = seq_lens.shape[0]
+    dev = _check_window("pa_prefill_window", q, k_pool, v_pool, block_tables, seq_lens, out, B,
+                        q_start)
+    _expect(q_start, "q_start", (B + 1,), torch.int32)
+    if T == 0 or B == 0:
+        return out
+    _call("pa_prefill_window", lib().pa_prefill_window, dev, stream, _ptr(q), _ptr(q_start), T,
+          int(max_q), _ptr(k_pool), _ptr(v_pool), _ptr(block_tables), block_tables.shape[1],
+          _ptr(seq_lens), B, Hq, Hkv, D, bs, NB, int(max_seq_len), float(scale), int(window),
+          int(sinks), _dtype(k_pool), _ptr(out), _dtype(out), ctypes.byref(plan.handle))
+    return out
 
 
 class BlockManager:

@@ -47,6 +47,7 @@ struct OccKey {
     int mq;
     int fused;
     int append;
+    int win;
 };
 
 size_t round_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
@@ -305,6 +306,7 @@ struct pa_plan {
     int last_fused = 0;
     size_t cnt_clean = 0;  // bytes at the end of the workspace known to be zero
     int last_path = 0, last_blocks = 0, last_warps = 0;
+    std::vector<void*> retired;  // workspaces that a windowed call outgrew, kept for captured graphs
     cudaEvent_t ev_start = nullptr, ev_stop = nullptr;
     MapKey kkey, vkey;
     CUtensorMap kmap, vmap;
@@ -352,15 +354,44 @@ pa_status pa_append_kv(const void* k_new, const void* v_new, void* k_pool, void*
 
 namespace {
 
+// Workspace of at least `need` bytes for a windowed call. Memory that a graph
+// captured with this plan may still use stays allocated until pa_free; during
+// a capture nothing can be allocated, and the call is refused instead.
+pa_status grow_workspace(pa_plan* plan, size_t need, cudaStream_t stream) {
+    if (plan->ws_bytes >= need) return PA_OK;
+    cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
+    if (cudaStreamIsCapturing(stream, &cap) != cudaSuccess) return PA_ERR_CUDA;
+    if (cap != cudaStreamCaptureStatusNone) return PA_ERR_WORKSPACE;
+    plan->retired.reserve(plan->retired.size() + 1);
+    void* ws = nullptr;
+    if (cudaMalloc(&ws, need) != cudaSuccess) {
+        cudaGetLastError();
+        return PA_ERR_CUDA;
+    }
+    // Zeroed in stream order (the piece counter starts at zero); the old
+    // memory is not touched, so calls in flight on it go on.
+    if (cudaMemsetAsync(ws, 0, need, stream) != cudaSuccess) {
+        cudaFree(ws);
+        return PA_ERR_CUDA;
+    }
+    if (plan->ws) plan->retired.push_back(plan->ws);
+    plan->ws = ws;
+    plan->ws_bytes = need;
+    plan->cnt_clean = need;
+    return PA_OK;
+}
+
 // The decode of pa_decode, with q_start != null (T query rows, at most nq per
 // sequence) of pa_decode_multi, and with k_new != null of pa_append_decode
-// (the step's new rows appended at position seq_lens[b] - 1 first).
+// (the step's new rows appended at position seq_lens[b] - 1 first). window > 0:
+// the sliding window of pa_decode_window, or with q_start of pa_prefill_window.
 pa_status decode_impl(const void* q, const int32_t* q_start, int T, int nq, const void* k_pool,
                       const void* v_pool, const int32_t* block_tables, int max_blocks,
                       const int32_t* seq_lens, int B, int Hq, int Hkv, int D, int block_size,
                       int num_blocks, int max_seq_len, float scale, pa_dtype kv_dtype, void* out,
                       pa_dtype out_dtype, pa_plan** plan_inout, struct CUstream_st* stream_,
-                      const void* k_new = nullptr, const void* v_new = nullptr) {
+                      const void* k_new = nullptr, const void* v_new = nullptr, int window = 0,
+                      int sinks = 0) {
     if (!q || !k_pool || !v_pool || !block_tables || !seq_lens || !out || !plan_inout)
         return PA_ERR_NULL;
     if (k_new && (!aligned16(k_new) || !aligned16(v_new))) return PA_ERR_ALIGN;
@@ -383,7 +414,7 @@ pa_status decode_impl(const void* q, const int32_t* q_start, int T, int nq, cons
     if (q_start) {
         if (kv_dtype != PA_BF16) return PA_ERR_DTYPE;
         if (T < 0 || nq < 1) return PA_ERR_SHAPE;
-        if (static_cast<int64_t>(nq) * (Hq / Hkv) > 16) {
+        if (window > 0 || static_cast<int64_t>(nq) * (Hq / Hkv) > 16) {
             const int gq = Hq / Hkv;
             if (D != 128 || gq > 128 || 128 % gq != 0 || max_blocks > 16384 ||
                 Hkv > pa::kMaxGridYZ)
@@ -399,7 +430,19 @@ pa_status decode_impl(const void* q, const int32_t* q_start, int T, int nq, cons
     // Everything that depends on the arguments alone is checked before a plan
     // exists, so that an argument error never creates one.
     const int g = Hq / Hkv;
-    int path = q_start ? PA_PATH_MMA : (*plan_inout ? (*plan_inout)->forced_path : PA_PATH_AUTO);
+    if (window > 0 && kv_dtype != PA_BF16) return PA_ERR_DTYPE;
+    // Tokens that any query sees, for the launch's sizes: the window, the
+    // sinks, and the rest of the pages they end in.
+    int vis_len = max_seq_len;
+    if (window > 0) {
+        const int limit = std::min(max_seq_len, max_blocks * block_size);
+        window = std::min(window, limit);
+        sinks = std::min(sinks, limit);
+        const int64_t rows = q_start ? std::min<int64_t>(nq, 128 / (Hq / Hkv)) : 1;
+        vis_len = static_cast<int>(std::min<int64_t>(
+            limit, static_cast<int64_t>(window) + sinks + rows + 2 * block_size));
+    }
+    int path = q_start || window > 0 ? PA_PATH_MMA : (*plan_inout ? (*plan_inout)->forced_path : PA_PATH_AUTO);
     // bf16 pools run on the tensor-core tile for every group size, one query
     // head per kv head included (one real column of eight: with the dynamic
     // tail it measured 94.9-95.0 us against 96.2 us for the CUDA-core path on
@@ -411,12 +454,17 @@ pa_status decode_impl(const void* q, const int32_t* q_start, int T, int nq, cons
     pa::SplitShape sh;
     if (path != PA_PATH_SIMPLE && !via_prefill &&
         !pa::split_shape(path == PA_PATH_FMA ? pa::kSplitFma : pa::kSplitMma, q_start ? nq : 0, B,
-                         Hq, Hkv, D, block_size, max_blocks, max_seq_len, &sh))
+                         Hq, Hkv, D, block_size, max_blocks, vis_len, &sh))
         return PA_ERR_SHAPE;
 
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return PA_ERR_CUDA;
     pa_plan* plan = *plan_inout;
+    if (!plan && window > 0) {  // a plan's memory cannot be allocated inside a capture
+        cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
+        if (cudaStreamIsCapturing(stream, &cap) != cudaSuccess) return PA_ERR_CUDA;
+        if (cap != cudaStreamCaptureStatusNone) return PA_ERR_WORKSPACE;
+    }
     if (!plan) {
         plan = new pa_plan();
         plan->device = dev;
@@ -442,11 +490,14 @@ pa_status decode_impl(const void* q, const int32_t* q_start, int T, int nq, cons
         // workspace after its first 64 bytes, which hold the split decode's
         // counters (zero between calls, left untouched here).
         const int64_t nqq = std::min<int64_t>(nq, T);
-        const int splits = pa::prefill_split_count(B, Hq, Hkv, nqq, max_seq_len, plan->num_sms);
+        const int splits = pa::prefill_split_count(B, Hq, Hkv, nqq, vis_len, plan->num_sms);
         float* part = nullptr;
         if (splits > 1) {
             const size_t need = 64 + pa::prefill_split_bytes(B, Hq, Hkv, nqq, splits);
-            if (plan->ws_bytes < need) {
+            if (window > 0) {
+                const pa_status st = grow_workspace(plan, need, stream);
+                if (st != PA_OK) return st;
+            } else if (plan->ws_bytes < need) {
                 if (plan->ws) cudaFree(plan->ws);
                 plan->ws = nullptr;
                 plan->ws_bytes = 0;
@@ -463,7 +514,7 @@ pa_status decode_impl(const void* q, const int32_t* q_start, int T, int nq, cons
                                                  out, plan->err, B, Hq, Hkv, max_blocks,
                                                  num_blocks, max_seq_len, nq, scale_log2,
                                                  out_dtype == PA_BF16, block_size, stream, part,
-                                                 splits, /*zero_invalid=*/1);
+                                                 splits, /*zero_invalid=*/1, window, sinks);
         if (plan->ev_stop) cudaEventRecord(plan->ev_stop, stream);
         plan->last_path = PA_PATH_PREFILL;
         plan->last_blocks = 0;
@@ -499,7 +550,8 @@ pa_status decode_impl(const void* q, const int32_t* q_start, int T, int nq, cons
     SplitLaunch L{sh.kind, D, block_size, sh.NT, sh.warps, 0, sh.smem};
     L.mq = sh.mq;
     // The fused merge serves one query per sequence on one n-tile.
-    const bool can_fuse = !q_start && sh.kind == pa::kSplitMma && sh.NT == 1 && sh.warps == 3;
+    L.win = window > 0 ? 1 : 0;
+    const bool can_fuse = !L.win && !q_start && sh.kind == pa::kSplitMma && sh.NT == 1 && sh.warps == 3;
     L.fused = can_fuse && plan->merge_mode == PA_MERGE_FUSED ? 1 : 0;
     if (plan->merge_mode == PA_MERGE_FUSED && !can_fuse) return PA_ERR_SHAPE;
     // The append rides in the split kernel on the one-n-tile tensor-core
@@ -514,15 +566,15 @@ pa_status decode_impl(const void* q, const int32_t* q_start, int T, int nq, cons
     for (const OccKey& o : plan->occ) {
         if (o.kind == L.kind && o.D == D && o.BS == block_size && o.NT == L.NT &&
             o.warps == L.warps && o.smem == L.smem && o.mq == L.mq && o.fused == L.fused &&
-            o.append == L.append)
+            o.append == L.append && o.win == L.win)
             per_sm = o.blocks_per_sm;
     }
     if (per_sm == 0) {
         cudaError_t e;
-        per_sm = pa::split_blocks_per_sm(L, &e);
+        per_sm = L.win ? pa::split_window_blocks_per_sm(L, &e) : pa::split_blocks_per_sm(L, &e);
         if (e != cudaSuccess || per_sm < 1) return PA_ERR_CUDA;
         plan->occ.push_back(OccKey{L.kind, D, block_size, L.NT, L.warps, L.smem, per_sm, L.mq,
-                                   L.fused, L.append});
+                                   L.fused, L.append, L.win});
     }
     pa::SplitGrid gr = pa::split_grid(sh, B, D, block_size,
                                       static_cast<int64_t>(q_start ? T : B) * Hq,
@@ -533,7 +585,10 @@ pa_status decode_impl(const void* q, const int32_t* q_start, int T, int nq, cons
 
     // Workspace: metadata, partial (m, l), partial value sums.
     const size_t need_ws = gr.workspace_bytes();
-    if (plan->ws_bytes < need_ws) {
+    if (L.win) {
+        const pa_status st = grow_workspace(plan, need_ws, stream);
+        if (st != PA_OK) return st;
+    } else if (plan->ws_bytes < need_ws) {
         if (plan->ws) cudaFree(plan->ws);
         plan->ws = nullptr;
         plan->ws_bytes = 0;
@@ -579,7 +634,7 @@ pa_status decode_impl(const void* q, const int32_t* q_start, int T, int nq, cons
         plan->vkey = vk;
     }
 
-    pa::SplitArgs a{};
+    pa::SplitWindowArgs a{};
     a.q = static_cast<const uint16_t*>(q);
     a.tables = block_tables;
     a.seq_lens = seq_lens;
@@ -603,6 +658,8 @@ pa_status decode_impl(const void* q, const int32_t* q_start, int T, int nq, cons
     a.num_q = T;
     a.probe_wait = pa::wait_probe();
     a.ws_cnt = cnt;
+    a.window = window;
+    a.sinks = sinks;
     if (L.append) {
         a.k_new = static_cast<const uint16_t*>(k_new);
         a.v_new = static_cast<const uint16_t*>(v_new);
@@ -613,7 +670,8 @@ pa_status decode_impl(const void* q, const int32_t* q_start, int T, int nq, cons
     }
 
     if (plan->ev_start) cudaEventRecord(plan->ev_start, stream);
-    cudaError_t e = pa::launch_split(L, plan->kmap, plan->vmap, a, stream);
+    cudaError_t e = L.win ? pa::launch_split_window(L, plan->kmap, plan->vmap, a, stream)
+                          : pa::launch_split(L, plan->kmap, plan->vmap, a, stream);
     if (plan->ev_stop) cudaEventRecord(plan->ev_stop, stream);
     if (e != cudaSuccess) return PA_ERR_CUDA;
     plan->last_fused = L.fused;
@@ -663,6 +721,41 @@ pa_status pa_decode_multi(const void* q, const int32_t* q_start, int num_queries
     return decode_impl(q, q_start, num_queries, max_q, k_pool, v_pool, block_tables, max_blocks,
                        seq_lens, B, Hq, Hkv, D, block_size, num_blocks, max_seq_len, scale, kv_dtype,
                        out, out_dtype, plan_inout, stream);
+}
+
+pa_status pa_decode_window(const void* q, const void* k_pool, const void* v_pool,
+                           const int32_t* block_tables, int max_blocks, const int32_t* seq_lens,
+                           int B, int Hq, int Hkv, int D, int block_size, int num_blocks,
+                           int max_seq_len, float scale, int window, int sinks, pa_dtype kv_dtype,
+                           void* out, pa_dtype out_dtype, pa_plan** plan_inout,
+                           struct CUstream_st* stream) {
+    if (window < 1 || sinks < 0) return PA_ERR_SHAPE;
+    try {
+        return decode_impl(q, nullptr, B, 1, k_pool, v_pool, block_tables, max_blocks, seq_lens, B,
+                           Hq, Hkv, D, block_size, num_blocks, max_seq_len, scale, kv_dtype, out,
+                           out_dtype, plan_inout, stream, nullptr, nullptr, window, sinks);
+    } catch (...) {  // host memory
+        return PA_ERR_CUDA;
+    }
+}
+
+pa_status pa_prefill_window(const void* q, const int32_t* q_start, int num_queries, int max_q,
+                            const void* k_pool, const void* v_pool, const int32_t* block_tables,
+                            int max_blocks, const int32_t* seq_lens, int B, int Hq, int Hkv, int D,
+                            int block_size, int num_blocks, int max_seq_len, float scale,
+                            int window, int sinks, pa_dtype kv_dtype, void* out,
+                            pa_dtype out_dtype, pa_plan** plan_inout, struct CUstream_st* stream) {
+    if (!q_start) return PA_ERR_NULL;
+    // The tiles' row maxima are taken before the scale: it must be positive.
+    if (window < 1 || sinks < 0 || !(scale > 0.f) || B > pa::kMaxGridYZ) return PA_ERR_SHAPE;
+    try {
+        return decode_impl(q, q_start, num_queries, max_q, k_pool, v_pool, block_tables, max_blocks,
+                           seq_lens, B, Hq, Hkv, D, block_size, num_blocks, max_seq_len, scale,
+                           kv_dtype, out, out_dtype, plan_inout, stream, nullptr, nullptr, window,
+                           sinks);
+    } catch (...) {  // host memory
+        return PA_ERR_CUDA;
+    }
 }
 
 pa_status pa_copy_blocks(void* k_pool, void* v_pool, const int32_t* copy_src,
@@ -724,6 +817,8 @@ pa_status pa_free(pa_plan* plan) {
     DeviceGuard guard(plan->device);
     pa_status st = PA_OK;
     if (plan->ws && cudaFree(plan->ws) != cudaSuccess) st = PA_ERR_CUDA;
+    for (void* p : plan->retired)
+        if (cudaFree(p) != cudaSuccess) st = PA_ERR_CUDA;
     if (plan->err && cudaFree(plan->err) != cudaSuccess) st = PA_ERR_CUDA;
     delete plan;
     return st;

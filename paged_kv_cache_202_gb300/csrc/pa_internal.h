@@ -90,6 +90,38 @@ struct SplitArgs {
     uint16_t* vpool_w;
 };
 
+// Arguments of the windowed split kernels (pa_decode_window): a token t of a
+// sequence of L is attended iff t >= L - window or t < sinks (both at most
+// max_seq_len). A parameter of its own: the plain kernels keep theirs.
+struct SplitWindowArgs : SplitArgs {
+    int window, sinks;
+};
+
+// The tokens that queries at positions first .. last of a sequence see with a
+// window W and S first tokens that stay visible: t <= p and (p - t < W or
+// t < S) for a query at p. The pages behind the sinks and before the window
+// hold none of them and are left out; what is left is numbered through
+// ("visible index" v): page v / BS of the visible ones is logical page p if
+// p < sink_pages, else p + skip. Visible index v is token v below the sink
+// pages' end and token v + skip * BS above it, and a query at position p sees
+//   v <= p - skip * BS  and  (v < S or v > p - skip * BS - W):
+// where pages are left out, indices S .. sink_pages * BS - 1 are at most
+// first - W - skip * BS, below every query's window, as their tokens are.
+struct WindowView {
+    int skip;   // pages left out between the sinks and the window
+    int len;    // visible indices up to and with token `last`
+    int lo;     // first visible index within the window of the query at `first`
+};
+__host__ __device__ inline WindowView window_view(int first, int last, int W, int S, int BS) {
+    const int w0 = first >= W ? first - W + 1 : 0;
+    const int skip = w0 / BS - (S + BS - 1) / BS;
+    WindowView v;
+    v.skip = skip > 0 ? skip : 0;
+    v.len = last + 1 - v.skip * BS;
+    v.lo = w0 - v.skip * BS;
+    return v;
+}
+
 struct SplitLaunch {
     int kind;      // SplitKind
     int D, BS, NT; // head dim, block size, n-tiles of 8 q heads (MMA)
@@ -99,6 +131,7 @@ struct SplitLaunch {
     int mq = 0;    // 1: several queries per sequence (tensor-core path only)
     int fused = 0; // 1: the split kernel merges its own partials (no merge kernel)
     int append = 0; // 1: the split kernel also appends the step's new K/V rows
+    int win = 0;   // 1: sliding window with sinks (tensor-core path, one query per sequence)
 };
 
 // Returns the resident blocks per SM of a split-kernel variant at the given
@@ -106,6 +139,11 @@ struct SplitLaunch {
 int split_blocks_per_sm(const SplitLaunch& L, cudaError_t* status);
 cudaError_t launch_split(const SplitLaunch& L, const CUtensorMap& kmap, const CUtensorMap& vmap,
                          const SplitArgs& a, cudaStream_t stream);
+// The same for the windowed kernels (L.win).
+int split_window_blocks_per_sm(const SplitLaunch& L, cudaError_t* status);
+cudaError_t launch_split_window(const SplitLaunch& L, const CUtensorMap& kmap,
+                                const CUtensorMap& vmap, const SplitWindowArgs& a,
+                                cudaStream_t stream);
 
 // Host-side planning of a split launch, shared by pa_decode,
 // pa_decode_multi and pa_decode_noalloc.
@@ -223,20 +261,22 @@ bool encode_query_map(CUtensorMap* map, const void* q, int T, int Hq, int g, int
 // run the one-tile kernel (pa_prefill_1t.cu), the others the two-tile
 // kernel. splits > 1 (one-tile kernel only) cuts every tile's key range into
 // that many blocks whose partials go to part (prefill_split_bytes) and are
-// merged by a second kernel.
+// merged by a second kernel. window > 0: a query at position p sees the tokens
+// t <= p with p - t < window or t < sinks (see WindowView).
 cudaError_t launch_prefill(const CUtensorMap& kmap, const CUtensorMap& vmap, const void* q,
                            int num_q, const int32_t* q_start, const int32_t* tables,
                            const int32_t* seq_lens, void* out, int* err, int B, int Hq, int Hkv,
                            int max_blocks, int num_blocks, int max_seq_len, int max_q,
                            float scale_log2, int out_bf16, int block_size, cudaStream_t stream,
-                           float* part = nullptr, int splits = 1, int zero_invalid = 0);
+                           float* part = nullptr, int splits = 1, int zero_invalid = 0,
+                           int window = 0, int sinks = 0);
 cudaError_t launch_prefill_one_tile(const CUtensorMap& kmap, const CUtensorMap& vmap, const void* q,
                                     int num_q, const int32_t* q_start, const int32_t* tables,
                                     const int32_t* seq_lens, void* out, int* err, int B, int Hq,
                                     int Hkv, int max_blocks, int num_blocks, int max_seq_len,
                                     int max_q, float scale_log2, int out_bf16, int block_size,
                                     cudaStream_t stream, float* part, int splits,
-                                    int zero_invalid);
+                                    int zero_invalid, int window, int sinks);
 // Key splits for a one-tile call (1: none) and the partial bytes they need;
 // nq = min(max_q, num_queries).
 int prefill_split_count(int B, int Hq, int Hkv, int64_t nq, int max_seq_len, int num_sms);

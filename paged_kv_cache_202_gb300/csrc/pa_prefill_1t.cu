@@ -48,6 +48,7 @@
 #include <cuda_bf16.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "pa.h"
 #include "pa_internal.h"
@@ -142,6 +143,12 @@ struct PrefillArgs {
     float* part;
 };
 
+// The window kernels' parameter: a longer one changes how the plain kernels
+// come out of the compiler (the one-tile kernel spilled).
+struct WindowPrefillArgs : PrefillArgs {
+    int window, sinks;
+};
+
 __device__ __forceinline__ void st_shared_v4(uint32_t addr, uint4 v) {
     asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z),
                  "r"(v.w)
@@ -200,10 +207,16 @@ __device__ void zero_rows(const PrefillArgs& a, int64_t r0, int64_t r1, int h0, 
     }
 }
 
-template <int BS>
+template <bool WIN>
+using KernelArgs = std::conditional_t<WIN, WindowPrefillArgs, PrefillArgs>;
+
+// WIN: sliding window with sinks. The block's chunks run over the visible
+// indices of its rows (WindowView): token limits, pages and masks below count
+// those, and `skip` maps a page to its logical one.
+template <int BS, bool WIN>
 __global__ void __launch_bounds__(kThreads, 1)
     prefill_one_tile_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
-                   const __grid_constant__ CUtensorMap qmap, const PrefillArgs a) {
+                   const __grid_constant__ CUtensorMap qmap, const KernelArgs<WIN> a) {
     extern __shared__ uint8_t smem_raw[];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t raw = smem_addr(smem_raw);
@@ -237,6 +250,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int limit = min(a.max_seq_len, a.max_blocks * BS);
     {
         const int64_t qs64 = a.q_start[b], n64 = static_cast<int64_t>(a.q_start[b + 1]) - qs64;
+        if (WIN && n64 == 0) return;  // a request without queries in this step
         if (n64 < 1 || n64 > a.max_q || L < n64 || L > limit || qs64 < 0 || qs64 + n64 > a.num_q) {
             if (blockIdx.x == 0 && h == 0 && tid == 0) atomicOr(a.err, kErrSeqLen);
             // The rows inside the arrays get zeros in a multi-query call and
@@ -253,7 +267,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int q0 = tile * a.Qb;
     if (q0 >= n) return;
     const int nq = min(a.Qb, n - q0);
-    const int ntok = L - n + q0 + nq;  // tokens the tile's last row sees
+    const int end = L - n + q0 + nq;  // tokens up to the tile's last row
+    int window = 0, sinks = 0;
+    WindowView view{0, 0, 0};
+    if constexpr (WIN) {
+        window = a.window;
+        sinks = a.sinks;
+        view = window_view(L - n + q0, end - 1, window, sinks, BS);
+    }
+    const int ntok = WIN ? view.len : end;  // tokens (visible indices) the tile's last row sees
+    auto logical = [&](int p) { return WIN && p >= (sinks + BS - 1) / BS ? p + view.skip : p; };
     const int nc = (ntok + kChunk - 1) / kChunk;
     const int nb = (ntok + BS - 1) / BS;
     const int32_t* table = a.tables + static_cast<size_t>(b) * a.max_blocks;
@@ -317,7 +340,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // The table entries this block reads, validated once.
     bool bad = false;
     for (int i = tid; i < nb; i += kThreads) {
-        const int p = table[i];
+        const int p = table[logical(i)];
         bad |= p < 0 || p >= a.num_blocks;
     }
     if (__syncthreads_or(bad)) {
@@ -374,7 +397,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int j = 0; j < kPages; ++j) {
                     const int p = c * kPages + j;
-                    pg[j] = p < nb ? table[p] : 0;
+                    pg[j] = p < nb ? table[logical(p)] : 0;
                 }
             };
             load_pages(c_beg);
@@ -498,7 +521,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         // is published in shared memory for the group that takes chunk c + 1.
         const uint32_t lane_base = static_cast<uint32_t>(32 * quarter + 16 * sub16) << 16;
         const uint32_t o_addr = tmem + lane_base + kColO;
-        const int pos_r = L - n + q0 + qi;  // last token this row sees
+        const int pos_r = L - n + q0 + qi - (WIN ? view.skip * BS : 0);  // last token (index) this row sees
+        const int lo_r = WIN ? pos_r - window : -1;   // from sinks to here: hidden from it
         float* mpub = reinterpret_cast<float*>(gbase + kOffM);
         float m_l = -INFINITY, l = 0.f;  // this thread's part of the row sum, in units of 2^m_l
         bool ok = true;
@@ -515,10 +539,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc::wait_ld();
             // Causal mask by predicate; the warp skips it when no row needs it.
             const int tok0 = c * kChunk + 64 * half;
-            if (!__all_sync(0xffffffffu, row_valid && c * kChunk + kChunk - 1 <= pos_r)) {
+            if (!__all_sync(0xffffffffu, row_valid && c * kChunk + kChunk - 1 <= pos_r &&
+                                             (!WIN || c * kChunk > lo_r || c * kChunk + kChunk <= sinks))) {
 #pragma unroll
                 for (int i = 0; i < kChunk / 2; ++i)
-                    sv[i] = (row_valid && tok0 + i <= pos_r) ? sv[i] : -INFINITY;
+                    sv[i] = (row_valid && tok0 + i <= pos_r &&
+                             (!WIN || tok0 + i > lo_r || tok0 + i < sinks)) ? sv[i] : -INFINITY;
             }
             // Row max: three-input max over pairs, four short chains, then the
             // partner's half.
@@ -591,8 +617,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             // Final chunk: zero the V rows past the last token before its
             // value product. The stage's previous chunk (c - 3) was consumed by
             // PV(c - 3), issued before S(c), so this parity wait is unambiguous.
-            if (c == nc - 1) {
-                const int valid = ntok - c * kChunk;
+            // With a window, also the rows between the sinks and the first
+            // row's window, which no row sees.
+            const int h0 = WIN ? max(0, sinks - c * kChunk) : 0;
+            const int h1 = WIN ? min(kChunk, view.lo - c * kChunk) : 0;
+            if (c == nc - 1 || h0 < h1) {
+                const int valid = WIN ? min(kChunk, ntok - c * kChunk) : ntok - c * kChunk;
                 ok = __all_sync(0xffffffffu, wait_role(bars + kBarVFull + 8 * (k % kStagesV),
                                                        (k / kStagesV) & 1, abort_flag, a.err));
                 if (!ok) break;
@@ -600,6 +630,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const uint32_t vst = base + kOffV + (k % kStagesV) * kStageKV;
                     for (int idx = tid % kGroupThreads; idx < (kChunk - valid) * 16; idx += kGroupThreads) {
                         const int r = valid + (idx >> 4), hf = (idx >> 3) & 1, ch = idx & 7;
+                        st_shared_v4(vst + hf * kHalfKV + r * 128 + ch * 16, make_uint4(0, 0, 0, 0));
+                    }
+                }
+                if constexpr (WIN) {
+                    const uint32_t vst = base + kOffV + (k % kStagesV) * kStageKV;
+                    for (int idx = tid % kGroupThreads; idx < (h1 - h0) * 16; idx += kGroupThreads) {
+                        const int r = h0 + (idx >> 4), hf = (idx >> 3) & 1, ch = idx & 7;
                         st_shared_v4(vst + hf * kHalfKV + r * 128 + ch * 16, make_uint4(0, 0, 0, 0));
                     }
                 }
@@ -764,8 +801,10 @@ cudaError_t launch_prefill_one_tile(const CUtensorMap& kmap, const CUtensorMap& 
                                     int Hkv, int max_blocks, int num_blocks, int max_seq_len,
                                     int max_q, float scale_log2, int out_bf16, int block_size,
                                     cudaStream_t stream, float* part, int splits,
-                                    int zero_invalid) {
-    PrefillArgs a{};
+                                    int zero_invalid, int window, int sinks) {
+    WindowPrefillArgs a{};
+    a.window = window;
+    a.sinks = sinks;
     a.q = static_cast<const uint16_t*>(q);
     a.q_start = q_start;
     a.tables = tables;
@@ -798,13 +837,20 @@ cudaError_t launch_prefill_one_tile(const CUtensorMap& kmap, const CUtensorMap& 
     dim3 grid(static_cast<unsigned>(tiles * splits), Hkv, B);
     CUtensorMap qmap;
     if (!encode_query_map(&qmap, q, num_q, Hq, a.g, a.Qb)) return cudaErrorInvalidValue;
-    auto kern = block_size == 16 ? prefill_one_tile_kernel<16> : prefill_one_tile_kernel<32>;
-    cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void*>(kern),
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         static_cast<int>(kSmemBytes));
-    if (e != cudaSuccess) return e;
-    kern<<<grid, kThreads, kSmemBytes, stream>>>(kmap, vmap, qmap, a);
-    e = cudaGetLastError();
+    auto launch = [&](auto kern, const auto& args) {
+        const cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void*>(kern),
+                                                   cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                   static_cast<int>(kSmemBytes));
+        if (e != cudaSuccess) return e;
+        kern<<<grid, kThreads, kSmemBytes, stream>>>(kmap, vmap, qmap, args);
+        return cudaGetLastError();
+    };
+    const cudaError_t e =
+        window > 0 ? launch(block_size == 16 ? prefill_one_tile_kernel<16, true>
+                                             : prefill_one_tile_kernel<32, true>, a)
+                   : launch(block_size == 16 ? prefill_one_tile_kernel<16, false>
+                                             : prefill_one_tile_kernel<32, false>,
+                            static_cast<const PrefillArgs&>(a));
     if (e != cudaSuccess || splits == 1) return e;
     SplitMergeArgs m{part, a.num_parts, q_start, seq_lens, out, out_bf16, B, Hq, Hkv, a.g, a.Qb,
                      a.tiles, splits, num_q, std::min(max_seq_len, max_blocks * block_size), max_q};

@@ -41,6 +41,8 @@
 //     O^T[D x 8 heads] += V^T[D x 16 tok] (P_hi^T + P_lo^T).
 #pragma once
 
+#include <type_traits>
+
 #include "pa_internal.h"
 #include "pa_ptx.cuh"
 
@@ -72,10 +74,16 @@ __device__ __forceinline__ void advance(Cursor& c, const int* pre, int U, int B)
 // several queries per sequence (q_start != null), a sequence is also invalid
 // unless it has 1 .. nq queries, at least as many tokens, and its query rows
 // lie within the num_q rows of q and out.
-template <int BS>
+// With a window (WIN), only the pages that hold a visible token count.
+template <int BS, bool WIN = false>
 __device__ void scan_lengths(const int32_t* __restrict__ seq_lens, int B, int limit, int* pre,
                              int* len, int* err, const int32_t* q_start = nullptr, int nq = 0,
-                             int num_q = 0) {
+                             int num_q = 0, int window = 0, int sinks = 0) {
+    auto pages = [&](int L) {
+        if constexpr (WIN)
+            if (L > 0) return (window_view(L - 1, L - 1, window, sinks, BS).len + BS - 1) / BS;
+        return (L + BS - 1) / BS;
+    };
     __shared__ int warp_tot[32];
     const int T = blockDim.x, tid = threadIdx.x;
     const int lane = tid & 31, warp = tid >> 5, nwarps = T >> 5;
@@ -92,7 +100,7 @@ __device__ void scan_lengths(const int32_t* __restrict__ seq_lens, int B, int li
         }
         bad |= !ok;
         len[b] = ok ? L : 0;
-        sum += ok ? (L + BS - 1) / BS : 0;
+        sum += ok ? pages(L) : 0;
     }
     if (bad && blockIdx.x == 0 && err) atomicOr(err, kErrSeqLen);
     int x = sum;
@@ -116,7 +124,7 @@ __device__ void scan_lengths(const int32_t* __restrict__ seq_lens, int B, int li
     int run = x - sum + (warp > 0 ? warp_tot[warp - 1] : 0);
     for (int b = lo; b < hi; ++b) {
         pre[b] = run;
-        run += (len[b] + BS - 1) / BS;
+        run += pages(len[b]);
     }
     if (tid == T - 1) pre[B] = run;
     __syncthreads();
@@ -308,11 +316,13 @@ struct MmaState {
     // nv: tokens of this chunk before the end of the sequence. With MQ, column
     // c of the tile is query c / g (of nqb, the newest tokens) and head c % g,
     // and query i sees only the tokens before rem - (nqb - 1 - i), rem being
-    // the tokens from the chunk's start to the end of the sequence.
-    template <bool MQ = false>
+    // the tokens from the chunk's start to the end of the sequence. With WIN,
+    // tokens h0 .. h1 - 1 of the chunk are hidden behind the window.
+    template <bool MQ = false, bool WIN = false>
     __device__ __forceinline__ void page(uint32_t kst, uint32_t vst, int nv, float scale_log2,
                                          int lane, int rem = 0, int nqb = 0, int g = 1,
-                                         uint32_t qst = 0, int nh = 0) {
+                                         uint32_t qst = 0, int nh = 0, int h0 = 0, int h1 = 0) {
+        auto seen = [&](int tk) { return tk < nv && (!WIN || tk < h0 || tk >= h1); };
         int lim[NT][2];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
@@ -378,7 +388,8 @@ struct MmaState {
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const int tk = tok + (i >= 2 ? 8 : 0);
-                    const float v = tk < lim[nt][i & 1] ? s[t][nt][i] * scale_log2 : -INFINITY;
+                    const bool in = tk < lim[nt][i & 1] && (!WIN || tk < h0 || tk >= h1);
+                    const float v = in ? s[t][nt][i] * scale_log2 : -INFINITY;
                     s[t][nt][i] = v;
                     mx[nt][i & 1] = fmaxf(mx[nt][i & 1], v);
                 }
@@ -450,7 +461,7 @@ struct MmaState {
                     for (int i = 0; i < 4; ++i) o[mt][nt][i] *= alpha[nt][i & 1];
         }
         // Values O^T += V^T P^T.
-        const bool tail = nv < BS;
+        const bool tail = nv < BS || (WIN && h0 < h1);
         const int t0 = 2 * (lane & 3);
 #pragma unroll
         for (int mt = 0; mt < KS; ++mt) {
@@ -461,8 +472,8 @@ struct MmaState {
                 ldsm_x4_trans(swz(vst, 2 * mt + ((lane >> 3) & 1), tok, BS), a0, a1, a2, a3);
                 if (tail) {
                     const int tb = t * 16 + t0;
-                    const uint32_t keep01 = (tb < nv ? 0x0000ffffu : 0u) | (tb + 1 < nv ? 0xffff0000u : 0u);
-                    const uint32_t keep89 = (tb + 8 < nv ? 0x0000ffffu : 0u) | (tb + 9 < nv ? 0xffff0000u : 0u);
+                    const uint32_t keep01 = (seen(tb) ? 0x0000ffffu : 0u) | (seen(tb + 1) ? 0xffff0000u : 0u);
+                    const uint32_t keep89 = (seen(tb + 8) ? 0x0000ffffu : 0u) | (seen(tb + 9) ? 0xffff0000u : 0u);
                     a0 &= keep01;
                     a1 &= keep01;
                     a2 &= keep89;
@@ -679,11 +690,18 @@ __device__ __forceinline__ void fold_segment(const SplitArgs& a, int x0, int x1,
 // head) into the pools. No other warp reads that slot in this call: every
 // page belongs to one range, and the other slices of a kv head patch their
 // own staged copies.
-template <int D, int BS, typename State, bool MQ = false, bool FUSED = false, bool APPEND = false>
+// WIN: sliding window with sinks. The page stream holds only the pages with a
+// visible token, numbered through (WindowView), so that the split, the
+// pipeline and the merge see shorter sequences; only the table lookup maps a
+// visible page to its logical one, and the chunks that the sinks' end or the
+// window's start cuts mask the tokens between.
+template <int D, int BS, typename State, bool MQ = false, bool FUSED = false, bool APPEND = false,
+          bool WIN = false>
 __device__ __forceinline__ void split_body(const CUtensorMap* kmap, const CUtensorMap* vmap,
-                                           const SplitArgs& a) {
+                                           const std::conditional_t<WIN, SplitWindowArgs, SplitArgs>& a) {
     static_assert(!(MQ && FUSED), "the fused merge serves one query per sequence");
     static_assert(!(APPEND && (MQ || FUSED)), "the fused append serves the plain decode");
+    static_assert(!(WIN && (MQ || FUSED || APPEND)), "the window serves the plain decode");
     static_assert(!MQ || State::kQS, "the multi-query tile reads its query rows from the stage");
     constexpr int CT = kChunkTokens;
     constexpr int CP = CT / BS;  // pages per chunk
@@ -720,6 +738,8 @@ __device__ __forceinline__ void split_body(const CUtensorMap* kmap, const CUtens
     const int limit = min(a.max_seq_len, a.max_blocks * BS);
     if constexpr (MQ)
         scan_lengths<BS>(a.seq_lens, a.B, limit, pre, len, a.err, a.q_start, a.nq, a.num_q);
+    else if constexpr (WIN)
+        scan_lengths<BS, true>(a.seq_lens, a.B, limit, pre, len, a.err, nullptr, 0, 0, a.window, a.sinks);
     else
         scan_lengths<BS>(a.seq_lens, a.B, limit, pre, len, a.err);
 
@@ -829,8 +849,12 @@ __device__ __forceinline__ void split_body(const CUtensorMap* kmap, const CUtens
         if (b != tb_row || pbase != tb_base) {
             tb_row = b;
             tb_base = pbase;
+            int left_out = 0;  // pages between the sinks and the window
+            if constexpr (WIN)
+                if (pbase + lane >= (a.sinks + BS - 1) / BS)
+                    left_out = window_view(len[b] - 1, len[b] - 1, a.window, a.sinks, BS).skip;
             tbl = (pbase + lane < nb)
-                      ? __ldg(a.tables + static_cast<size_t>(b) * a.max_blocks + pbase + lane)
+                      ? __ldg(a.tables + static_cast<size_t>(b) * a.max_blocks + pbase + lane + left_out)
                       : -1;
         }
         return __shfl_sync(0xffffffffu, tbl, p - pbase);
@@ -1007,11 +1031,21 @@ __device__ __forceinline__ void split_body(const CUtensorMap* kmap, const CUtens
         if ((badmask >> s) & 1u) {
             poison = true;
         } else {
-            const int rem = len[cc.b] - cc.p * BS;  // tokens from the chunk start to the end
+            int Lb = len[cc.b], h0 = 0, h1 = 0;
+            if constexpr (WIN) {
+                const WindowView w = window_view(Lb - 1, Lb - 1, a.window, a.sinks, BS);
+                Lb = w.len;
+                h0 = max(0, min(CT, a.sinks - cc.p * BS));
+                h1 = max(0, min(CT, w.lo - cc.p * BS));
+            }
+            const int rem = Lb - cc.p * BS;  // tokens from the chunk start to the end
             const int nv = min(n * BS, rem);
             if constexpr (MQ)
                 st.template page<true>(stg, stg + CT * D * 2, nv, a.scale_log2, lane, rem, nqb, a.g,
                                        stg + 2 * CT * D * 2, nh);
+            else if constexpr (WIN)
+                st.template page<false, true>(stg, stg + CT * D * 2, nv, a.scale_log2, lane, 0, 0, 1, my_q,
+                                              nh, h0, h1);
             else if constexpr (State::kQS)
                 st.page(stg, stg + CT * D * 2, nv, a.scale_log2, lane, 0, 0, 1, my_q, nh);
             else
