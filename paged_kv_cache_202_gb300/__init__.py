@@ -457,52 +457,60 @@ class Rope:
         self.address = ctypes.addressof(self.struct)   # what the calls pass; the struct stays with self
 
 
-def _one_device(what: str, ts) -> torch.device:
-    """The CUDA device that all given tensors are on."""
-    dev = ts[0].device
-    for t in ts:
-        if t.device != dev:
-            raise ValueError(f"{what}: tensors on {dev} and {t.device}: all must be on one device")
-    if dev.type != "cuda":
-        raise ValueError(f"{what}: tensors must be on a CUDA device")
-    return dev
+# A decode step makes these calls once a layer, on a few rows: the checks are
+# what the call costs. Each argument is checked in one expression of attribute
+# reads that is true for what the call takes; _refuse then finds out what is
+# wrong with one that is not. (One call of pa_step_maps: 17 us with a helper
+# per property and torch.cuda.current_stream, of which the library's call is
+# 3.5 us; 9 us this way.)
+
+def _refuse(what: str, name: str, t: torch.Tensor, dev: int, shape: tuple, dtype: torch.dtype):
+    if not t.is_cuda:
+        raise ValueError(f"{what}: {name}: tensors must be on a CUDA device")
+    if t.get_device() != dev:
+        raise ValueError(f"{what}: {name} is on {t.device}, not on device {dev}: all must be on one device")
+    if t.dtype != dtype:
+        raise TypeError(f"{what}: {name} is {t.dtype}, expected {dtype}")
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{what}: {name} has shape {tuple(t.shape)}, expected {shape}")
+    raise ValueError(f"{what}: {name} must be contiguous")
 
 
-def _call(what: str, fn, dev: torch.device, stream, *args) -> None:
-    """Call fn(*args, stream) with dev current, on its current stream by default."""
+def _call(what: str, fn, dev: int, stream, *args) -> None:
+    """fn(*args, stream) with device dev current, on its current stream by default."""
     if stream is None:
-        stream = torch.cuda.current_stream(dev).cuda_stream
+        stream = torch._C._cuda_getCurrentRawStream(dev)
     elif hasattr(stream, "cuda_stream"):
         stream = stream.cuda_stream
-    if dev.index == torch.cuda.current_device():
+    if dev == torch.cuda.current_device():
         st = fn(*args, stream)
     else:
         with torch.cuda.device(dev):
             st = fn(*args, stream)
-    if st != PA_OK:
+    if st:
         raise PagedAttentionError(st, what)
 
 
-def _rows(t: torch.Tensor, name: str, shape: tuple, dtype: torch.dtype) -> tuple[int, int]:
-    """(address, row stride) of [rows, H, D] rows whose heads are contiguous."""
-    if tuple(t.shape) != shape:
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {shape}")
-    if t.dtype != dtype:
-        raise TypeError(f"{name} is {t.dtype}, expected {dtype}")
+def _rows(what: str, name: str, t: torch.Tensor, dev: int, shape: tuple, dtype: torch.dtype) -> int:
+    """The row stride of [rows, H, D] rows whose heads are contiguous."""
+    if t.dtype is not dtype or t.get_device() != dev or t.shape != shape:
+        _refuse(what, name, t, dev, shape, dtype)
     T, H, D = shape
     s0, s1, s2 = t.stride()
-    if s2 != 1 or (H > 1 and s1 != D):
-        raise ValueError(f"{name}: the heads of a row must be contiguous")
-    return t.data_ptr(), (s0 if T > 1 else H * D)
+    if s2 != 1 or (s1 != D and H > 1):
+        raise ValueError(f"{what}: {name}: the heads of a row must be contiguous")
+    return s0 if T > 1 else H * D
 
 
-def _vector(t: torch.Tensor, name: str, n: int, dtype: torch.dtype) -> int:
-    if t.dtype != dtype:
-        raise TypeError(f"{name} is {t.dtype}, expected {dtype}")
-    if t.dim() != 1 or t.shape[0] != n:
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected ({n},)")
-    if n > 1 and t.stride(0) != 1:
-        raise ValueError(f"{name} must be contiguous")
+_I32, _I64 = torch.int32, torch.int64
+_INT_MAX = 2 ** 31 - 1   # a C int would drop the upper bits of more; bounds and windows saturate
+
+
+def _weight(what: str, name: str, t: torch.Tensor | None, dev: int, D: int, dtype: torch.dtype) -> int | None:
+    if t is None:
+        return None
+    if t.dtype is not dtype or t.get_device() != dev or t.shape != (D,) or not t.is_contiguous():
+        _refuse(what, name, t, dev, (D,), dtype)
     return t.data_ptr()
 
 
@@ -518,22 +526,33 @@ def pa_step_maps(cache_lens: torch.Tensor, new_lens: torch.Tensor, free_blocks: 
     ``free_blocks`` is a stack of free block ids of which ``free_count`` [1]
     are valid; ``slots`` may have more rows than the step (padding: slot -1).
     """
-    i32 = torch.int32
-    B, T = cache_lens.shape[0], slots.shape[0]
-    ts = [cache_lens, new_lens, free_blocks, free_count, block_tables, seq_lens, q_start, positions,
-          slots, free_left]
+    what = "pa_step_maps"
+    B, T, F = cache_lens.shape[0], slots.shape[0], free_blocks.shape[0]
+    MB = block_tables.shape[-1]
+    dev = cache_lens.get_device()
+    for name, t, shape in (("cache_lens", cache_lens, (B,)), ("new_lens", new_lens, (B,)),
+                           ("free_blocks", free_blocks, (F,)), ("free_count", free_count, (1,)),
+                           ("block_tables", block_tables, (B, MB)), ("seq_lens", seq_lens, (B,)),
+                           ("q_start", q_start, (B + 1,)), ("positions", positions, (T,)),
+                           ("free_left", free_left, (1,))):
+        if t.dtype is not _I32 or t.get_device() != dev or t.shape != shape or not t.is_contiguous():
+            _refuse(what, name, t, dev, shape, _I32)
+    if slots.dtype is not _I64 or slots.get_device() != dev or not slots.is_contiguous() or slots.dim() != 1:
+        _refuse(what, "slots", slots, dev, (T,), _I64)
+    if dev < 0:
+        _refuse(what, "cache_lens", cache_lens, dev, (B,), _I32)
+    if T > _INT_MAX or F > _INT_MAX or B > _INT_MAX:
+        raise ValueError(f"{what}: more than 2^31 - 1 rows, free blocks or requests")
+    err = None
     if device_error is not None:
-        ts.append(device_error)
-    dev = _one_device("pa_step_maps", ts)
-    _expect(block_tables, "block_tables", (B, block_tables.shape[-1]), i32)
-    _call("pa_step_maps", lib().pa_step_maps, dev, stream,
-          _vector(cache_lens, "cache_lens", B, i32), _vector(new_lens, "new_lens", B, i32), B,
-          _vector(free_blocks, "free_blocks", free_blocks.shape[0], i32) or free_count.data_ptr(),
-          free_blocks.shape[0], _vector(free_count, "free_count", 1, i32), _ptr(block_tables),
-          block_tables.shape[1], int(block_size), int(num_blocks), int(max_seq_len),
-          _vector(seq_lens, "seq_lens", B, i32), _vector(q_start, "q_start", B + 1, i32),
-          _vector(positions, "positions", T, i32), _vector(slots, "slots", T, torch.int64), T,
-          _vector(free_left, "free_left", 1, i32), _error_word(device_error))
+        err = _error_word(device_error)
+        if device_error.get_device() != dev:
+            _refuse(what, "device_error", device_error, dev, (1,), _I32)
+    _call(what, lib().pa_step_maps, dev, stream, cache_lens.data_ptr(), new_lens.data_ptr(), B,
+          free_blocks.data_ptr() or free_count.data_ptr(), F, free_count.data_ptr(),
+          block_tables.data_ptr(), MB, int(block_size), int(num_blocks), min(int(max_seq_len), _INT_MAX),
+          seq_lens.data_ptr(),
+          q_start.data_ptr(), positions.data_ptr(), slots.data_ptr(), T, free_left.data_ptr(), err)
 
 
 def pa_qk_rope(q: torch.Tensor, k: torch.Tensor, positions: torch.Tensor, rope: Rope | None,
@@ -542,27 +561,23 @@ def pa_qk_rope(q: torch.Tensor, k: torch.Tensor, positions: torch.Tensor, rope: 
     """Norm (where a weight is given) and rotate ``q`` [T, Hq, D] and ``k`` [T, Hk, D]
     into ``q_out`` and ``k_out``, which may be the inputs themselves. Rows may
     be strided (views of a fused projection); the heads of a row are contiguous."""
-    T, Hq, D = q.shape
+    what = "pa_qk_rope"
+    T, Hq, D = shape = q.shape
     Hk = k.shape[1]
     dt = q.dtype
-    ts = [q, k, positions, q_out, k_out]
-    qw = kw = None
-    if q_weight is not None:
-        ts.append(q_weight)
-        qw = _vector(q_weight, "q_weight", D, dt)
-    if k_weight is not None:
-        ts.append(k_weight)
-        kw = _vector(k_weight, "k_weight", D, dt)
-    dev = _one_device("pa_qk_rope", ts)
-    qp, qs = _rows(q, "q", (T, Hq, D), dt)
-    kp, ks = _rows(k, "k", (T, Hk, D), dt)
-    qo, qos = _rows(q_out, "q_out", (T, Hq, D), dt)
-    ko, kos = _rows(k_out, "k_out", (T, Hk, D), dt)
+    dev = q.get_device()
+    qs, qos = _rows(what, "q", q, dev, shape, dt), _rows(what, "q_out", q_out, dev, shape, dt)
+    shape = (T, Hk, D)
+    ks, kos = _rows(what, "k", k, dev, shape, dt), _rows(what, "k_out", k_out, dev, shape, dt)
+    if (positions.dtype is not _I32 or positions.get_device() != dev or positions.shape != (T,)
+            or not positions.is_contiguous() or dev < 0):
+        _refuse(what, "positions", positions, dev, (T,), _I32)
     if T == 0:
         return
-    _call("pa_qk_rope", lib().pa_qk_rope, dev, stream, qp, qs, kp, ks,
-          _vector(positions, "positions", T, torch.int32), T, Hq, Hk, D, _dtype(q), qw, kw,
-          float(eps), rope.address if rope is not None else None, qo, qos, ko, kos)
+    _call(what, lib().pa_qk_rope, dev, stream, q.data_ptr(), qs, k.data_ptr(), ks,
+          positions.data_ptr(), T, Hq, Hk, D, _dtype(q), _weight(what, "q_weight", q_weight, dev, D, dt),
+          _weight(what, "k_weight", k_weight, dev, D, dt), float(eps),
+          None if rope is None else rope.address, q_out.data_ptr(), qos, k_out.data_ptr(), kos)
 
 
 def pa_qk_rope_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, positions: torch.Tensor,
@@ -573,43 +588,55 @@ def pa_qk_rope_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, positio
                       stream=None) -> None:
     """``pa_qk_rope`` with the keys and values written to the paged pools at
     ``slots`` (int64 [T]; -1 marks a padding row, which is left alone)."""
-    T, Hq, D = q.shape
-    NB, Hkv, bs, _ = _pools(k_pool, v_pool)
+    what = "pa_qk_rope_append"
+    T, Hq, D = shape = q.shape
+    NB, Hkv, bs, _ = pool = k_pool.shape
     dt = q.dtype
-    ts = [q, k, v, positions, slots, k_pool, v_pool, q_out]
-    qw = kw = None
-    if q_weight is not None:
-        ts.append(q_weight)
-        qw = _vector(q_weight, "q_weight", D, dt)
-    if k_weight is not None:
-        ts.append(k_weight)
-        kw = _vector(k_weight, "k_weight", D, dt)
+    dev = q.get_device()
+    qs, qos = _rows(what, "q", q, dev, shape, dt), _rows(what, "q_out", q_out, dev, shape, dt)
+    shape = (T, Hkv, D)
+    ks, vs = _rows(what, "k", k, dev, shape, dt), _rows(what, "v", v, dev, shape, dt)
+    pool = (NB, Hkv, bs, D)
+    for name, t in (("k_pool", k_pool), ("v_pool", v_pool)):
+        if t.dtype is not dt or t.get_device() != dev or t.shape != pool or not t.is_contiguous():
+            _refuse(what, name, t, dev, pool, dt)
+    if (positions.dtype is not _I32 or positions.get_device() != dev or positions.shape != (T,)
+            or not positions.is_contiguous() or dev < 0):
+        _refuse(what, "positions", positions, dev, (T,), _I32)
+    if (slots.dtype is not _I64 or slots.get_device() != dev or slots.shape != (T,)
+            or not slots.is_contiguous()):
+        _refuse(what, "slots", slots, dev, (T,), _I64)
+    err = None
     if device_error is not None:
-        ts.append(device_error)
-    dev = _one_device("pa_qk_rope_append", ts)
-    _expect(k_pool, "k_pool", (NB, Hkv, bs, D), dt)
-    qp, qs = _rows(q, "q", (T, Hq, D), dt)
-    kp, ks = _rows(k, "k", (T, Hkv, D), dt)
-    vp, vs = _rows(v, "v", (T, Hkv, D), dt)
-    qo, qos = _rows(q_out, "q_out", (T, Hq, D), dt)
+        err = _error_word(device_error)
+        if device_error.get_device() != dev:
+            _refuse(what, "device_error", device_error, dev, (1,), _I32)
     if T == 0:
         return
-    _call("pa_qk_rope_append", lib().pa_qk_rope_append, dev, stream, qp, qs, kp, ks, vp, vs,
-          _vector(positions, "positions", T, torch.int32), _vector(slots, "slots", T, torch.int64),
-          T, Hq, Hkv, D, _dtype(q), qw, kw, float(eps), rope.address if rope is not None else None,
-          qo, qos, _ptr(k_pool), _ptr(v_pool), bs, NB, _error_word(device_error))
+    _call(what, lib().pa_qk_rope_append, dev, stream, q.data_ptr(), qs, k.data_ptr(), ks,
+          v.data_ptr(), vs, positions.data_ptr(), slots.data_ptr(), T, Hq, Hkv, D, _dtype(q),
+          _weight(what, "q_weight", q_weight, dev, D, dt),
+          _weight(what, "k_weight", k_weight, dev, D, dt), float(eps),
+          None if rope is None else rope.address, q_out.data_ptr(), qos, k_pool.data_ptr(),
+          v_pool.data_ptr(), bs, NB, err)
 
 
-def _check_window(what, q, k_pool, v_pool, block_tables, seq_lens, out, B: int, *more) -> tuple:
-    dev = _one_device(what, (q, k_pool, v_pool, block_tables, seq_lens, out, *more))
-    if q.dtype != k_pool.dtype:
-        raise TypeError(f"q is {q.dtype}, the pools are {k_pool.dtype}")
-    if q.shape[2] != k_pool.shape[3]:
-        raise ValueError(f"q has {q.shape[2]} elements a head, the pools {k_pool.shape[3]}")
-    _expect(out, "out", tuple(q.shape))
-    _expect(block_tables, "block_tables", (B, block_tables.shape[-1]), torch.int32)
-    _expect(seq_lens, "seq_lens", (B,), torch.int32)
-    return dev
+def _check_window(what: str, q, k_pool, v_pool, block_tables, seq_lens, out, B: int) -> tuple:
+    """Devices, types and shapes of a windowed call: (device, Hkv, block size, blocks)."""
+    T, Hq, D = shape = q.shape
+    NB, Hkv, bs, _ = k_pool.shape
+    pool, MB, dt, dev = (NB, Hkv, bs, D), block_tables.shape[-1], q.dtype, q.get_device()
+    for name, t in (("k_pool", k_pool), ("v_pool", v_pool)):
+        if t.dtype is not dt or t.get_device() != dev or t.shape != pool or not t.is_contiguous():
+            _refuse(what, name, t, dev, pool, dt)
+    if out.get_device() != dev or out.shape != shape or not out.is_contiguous():
+        _refuse(what, "out", out, dev, tuple(shape), out.dtype)
+    if not q.is_contiguous() or dev < 0:
+        _refuse(what, "q", q, dev, tuple(shape), dt)
+    for name, t, shape in (("block_tables", block_tables, (B, MB)), ("seq_lens", seq_lens, (B,))):
+        if t.dtype is not _I32 or t.get_device() != dev or t.shape != shape or not t.is_contiguous():
+            _refuse(what, name, t, dev, shape, _I32)
+    return dev, MB, NB, Hkv, bs
 
 
 def pa_decode_window(q: torch.Tensor, k_pool: torch.Tensor, v_pool: torch.Tensor,
@@ -620,12 +647,13 @@ def pa_decode_window(q: torch.Tensor, k_pool: torch.Tensor, v_pool: torch.Tensor
     ``sinks`` tokens of every sequence into ``out``; returns ``out`` (bf16 pools).
     Table entries of pages between the two are never read."""
     B, Hq, D = q.shape
-    NB, Hkv, bs, _ = _pools(k_pool, v_pool)
-    dev = _check_window("pa_decode_window", q, k_pool, v_pool, block_tables, seq_lens, out, B)
-    _call("pa_decode_window", lib().pa_decode_window, dev, stream, _ptr(q), _ptr(k_pool),
-          _ptr(v_pool), _ptr(block_tables), block_tables.shape[1], _ptr(seq_lens), B, Hq, Hkv, D,
-          bs, NB, int(max_seq_len), float(scale), int(window), int(sinks), _dtype(k_pool),
-          _ptr(out), _dtype(out), ctypes.byref(plan.handle))
+    dev, MB, NB, Hkv, bs = _check_window("pa_decode_window", q, k_pool, v_pool, block_tables,
+                                         seq_lens, out, B)
+    _call("pa_decode_window", lib().pa_decode_window, dev, stream, q.data_ptr(),
+          k_pool.data_ptr(), v_pool.data_ptr(), block_tables.data_ptr(), MB, seq_lens.data_ptr(), B,
+          Hq, Hkv, D, bs, NB, min(int(max_seq_len), _INT_MAX), float(scale), min(int(window), _INT_MAX),
+          min(int(sinks), _INT_MAX), _dtype(q), out.data_ptr(),
+          _dtype(out), ctypes.byref(plan.handle))
     return out
 
 
@@ -635,18 +663,20 @@ def pa_prefill_window(q: torch.Tensor, q_start: torch.Tensor, k_pool: torch.Tens
                       max_seq_len: int, plan: Plan, stream=None) -> torch.Tensor:
     """``pa_decode_window`` for the newest queries of every sequence (rows as for
     ``pa_prefill``; bf16 pools, D = 128); returns ``out``."""
+    what = "pa_prefill_window"
     T, Hq, D = q.shape
-    NB, Hkv, bs, _ = _pools(k_pool, v_pool)
     B = seq_lens.shape[0]
-    dev = _check_window("pa_prefill_window", q, k_pool, v_pool, block_tables, seq_lens, out, B,
-                        q_start)
-    _expect(q_start, "q_start", (B + 1,), torch.int32)
+    dev, MB, NB, Hkv, bs = _check_window(what, q, k_pool, v_pool, block_tables, seq_lens, out, B)
+    if (q_start.dtype is not _I32 or q_start.get_device() != dev or q_start.shape != (B + 1,)
+            or not q_start.is_contiguous()):
+        _refuse(what, "q_start", q_start, dev, (B + 1,), _I32)
     if T == 0 or B == 0:
         return out
-    _call("pa_prefill_window", lib().pa_prefill_window, dev, stream, _ptr(q), _ptr(q_start), T,
-          int(max_q), _ptr(k_pool), _ptr(v_pool), _ptr(block_tables), block_tables.shape[1],
-          _ptr(seq_lens), B, Hq, Hkv, D, bs, NB, int(max_seq_len), float(scale), int(window),
-          int(sinks), _dtype(k_pool), _ptr(out), _dtype(out), ctypes.byref(plan.handle))
+    _call(what, lib().pa_prefill_window, dev, stream, q.data_ptr(), q_start.data_ptr(), T, max_q,
+          k_pool.data_ptr(), v_pool.data_ptr(), block_tables.data_ptr(), MB, seq_lens.data_ptr(), B,
+          Hq, Hkv, D, bs, NB, min(int(max_seq_len), _INT_MAX), float(scale), min(int(window), _INT_MAX),
+          min(int(sinks), _INT_MAX), _dtype(q), out.data_ptr(),
+          _dtype(out), ctypes.byref(plan.handle))
     return out
 
 

@@ -134,6 +134,36 @@ __global__ void __launch_bounds__(32 * kRopeWarps) rope_kernel(const __grid_cons
         r0 = v0 * N < a.rot;
         r1 = v1 * N < a.rot;
     }
+    struct Group {       // this thread's part of a group of heads
+        uint4 w0, w1;
+        T* dst;
+        int kind;        // 0: q, 1: k, 2: v, 3: no head
+    };
+    auto load = [&](int g) {
+        const int head = g * HPW + lane / TPH;
+        Group r;
+        r.kind = head < a.Hq ? 0 : head < a.Hq + a.Hk ? 1 : head < heads ? 2 : 3;
+        const int h = head - (r.kind == 0 ? 0 : r.kind == 1 ? a.Hq : a.Hq + a.Hk);
+        r.w0 = r.w1 = make_uint4(0, 0, 0, 0);
+        r.dst = nullptr;
+        if (r.kind < 3) {
+            const T* src = static_cast<const T*>(r.kind == 0 ? a.q : r.kind == 1 ? a.k : a.v) +
+                           static_cast<int64_t>(t) * (r.kind == 0 ? a.q_stride : r.kind == 1 ? a.k_stride : a.v_stride) +
+                           h * D;
+            r.w0 = *reinterpret_cast<const uint4*>(src + v0 * N);
+            r.w1 = *reinterpret_cast<const uint4*>(src + v1 * N);
+            if (r.kind == 0) {
+                r.dst = static_cast<T*>(a.q_out) + static_cast<int64_t>(t) * a.qo_stride + h * D;
+            } else if constexpr (APPEND) {
+                r.dst = static_cast<T*>(r.kind == 1 ? a.kpool : a.vpool) +
+                        ((((slot >> a.shift) * a.Hk + h) << a.shift) + (slot & ((1 << a.shift) - 1))) * D;
+            } else {
+                r.dst = static_cast<T*>(a.k_out) + static_cast<int64_t>(t) * a.ko_stride + h * D;
+            }
+        }
+        return r;
+    };
+    Group next = load(g0);
     float2 sc[N];  // sin, cos: pair by pair
 #pragma unroll
     for (int i = 0; i < N; ++i) {
@@ -146,34 +176,15 @@ __global__ void __launch_bounds__(32 * kRopeWarps) rope_kernel(const __grid_cons
             sc[i].y *= a.amplitude;
         }
     }
+    // The vectors of the next group are on their way while one is worked on.
     for (int g = g0; g < g1; ++g) {
-        const int head = g * HPW + lane / TPH;
-        const bool is_q = head < a.Hq, is_k = !is_q && head < a.Hq + a.Hk;
-        const bool on = head < heads;
-        const T* src = nullptr;
-        T* dst = nullptr;
-        if (on) {
-            const int h = is_q ? head : is_k ? head - a.Hq : head - a.Hq - a.Hk;
-            src = static_cast<const T*>(is_q ? a.q : is_k ? a.k : a.v) +
-                  static_cast<int64_t>(t) * (is_q ? a.q_stride : is_k ? a.k_stride : a.v_stride) + h * D;
-            if (is_q) {
-                dst = static_cast<T*>(a.q_out) + static_cast<int64_t>(t) * a.qo_stride + h * D;
-            } else if constexpr (APPEND) {
-                dst = static_cast<T*>(is_k ? a.kpool : a.vpool) +
-                      ((((slot >> a.shift) * a.Hk + h) << a.shift) + (slot & ((1 << a.shift) - 1))) * D;
-            } else {
-                dst = static_cast<T*>(a.k_out) + static_cast<int64_t>(t) * a.ko_stride + h * D;
-            }
-        }
-        uint4 w0 = make_uint4(0, 0, 0, 0), w1 = w0;
-        if (on) {
-            w0 = *reinterpret_cast<const uint4*>(src + v0 * N);
-            w1 = *reinterpret_cast<const uint4*>(src + v1 * N);
-        }
-        const T* weight = static_cast<const T*>(is_q ? a.q_weight : is_k ? a.k_weight : nullptr);
+        const Group now = next;
+        if (g + 1 < g1) next = load(g + 1);
+        const bool is_q = now.kind == 0, turn = now.kind <= 1;
+        const T* weight = static_cast<const T*>(is_q ? a.q_weight : now.kind == 1 ? a.k_weight : nullptr);
         float x[2 * N];
-        Vec<T>::unpack(w0, x);
-        Vec<T>::unpack(w1, x + N);
+        Vec<T>::unpack(now.w0, x);
+        Vec<T>::unpack(now.w1, x + N);
         const bool norm = weight != nullptr;
         if (__any_sync(0xffffffffu, norm)) {
             float ss = 0.f;
@@ -190,7 +201,6 @@ __global__ void __launch_bounds__(32 * kRopeWarps) rope_kernel(const __grid_cons
                 for (int i = 0; i < 2 * N; ++i) x[i] *= r * wt[i];
             }
         }
-        const bool turn = is_q || is_k;
 #pragma unroll
         for (int i = 0; i < N; ++i) {
             const int e1 = HALF ? i : 2 * i, e2 = HALF ? i + N : 2 * i + 1;
@@ -202,11 +212,11 @@ __global__ void __launch_bounds__(32 * kRopeWarps) rope_kernel(const __grid_cons
             }
         }
         // A vector that is neither normalised nor rotated keeps its bits.
-        if (norm || (turn && r0)) w0 = Vec<T>::pack(x);
-        if (norm || (turn && r1)) w1 = Vec<T>::pack(x + N);
-        if (on) {
-            *reinterpret_cast<uint4*>(dst + v0 * N) = w0;
-            *reinterpret_cast<uint4*>(dst + v1 * N) = w1;
+        const uint4 w0 = norm || (turn && r0) ? Vec<T>::pack(x) : now.w0;
+        const uint4 w1 = norm || (turn && r1) ? Vec<T>::pack(x + N) : now.w1;
+        if (now.kind < 3) {
+            *reinterpret_cast<uint4*>(now.dst + v0 * N) = w0;
+            *reinterpret_cast<uint4*>(now.dst + v1 * N) = w1;
         }
     }
 }
