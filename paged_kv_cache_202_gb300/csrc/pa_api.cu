@@ -381,6 +381,16 @@ pa_status grow_workspace(pa_plan* plan, size_t need, cudaStream_t stream) {
     return PA_OK;
 }
 
+// Which kernel a windowed multi-query call runs: the persistent one over pairs
+// of tiles, or (few tiles, or one tile a sequence) the one-tile kernel with its
+// key split.
+bool window_items(int B, int Hq, int Hkv, int64_t nq, int num_sms) {
+    const int qb = 128 / (Hq / Hkv);
+    const int force = pa::prefill_kernel_choice();  // a test may pin either kernel
+    if (force != PA_PREFILL_AUTO) return force == PA_PREFILL_TWO_TILE;
+    return nq > qb && (nq + qb - 1) / qb * static_cast<int64_t>(Hkv) * B > 3LL * num_sms;
+}
+
 // The decode of pa_decode, with q_start != null (T query rows, at most nq per
 // sequence) of pa_decode_multi, and with k_new != null of pa_append_decode
 // (the step's new rows appended at position seq_lens[b] - 1 first). window > 0:
@@ -490,6 +500,23 @@ pa_status decode_impl(const void* q, const int32_t* q_start, int T, int nq, cons
         // workspace after its first 64 bytes, which hold the split decode's
         // counters (zero between calls, left untouched here).
         const int64_t nqq = std::min<int64_t>(nq, T);
+        if (window > 0 && window_items(B, Hq, Hkv, nqq, plan->num_sms)) {
+            const size_t need = 64 + pa::prefill_window_bytes(B, Hq, Hkv, T);
+            const pa_status st = grow_workspace(plan, need, stream);
+            if (st != PA_OK) return st;
+            plan->cnt_clean = std::min(plan->cnt_clean, plan->ws_bytes - need);
+            if (plan->ev_start) cudaEventRecord(plan->ev_start, stream);
+            const cudaError_t e = pa::launch_prefill_window(
+                kmap, vmap, q, T, q_start, block_tables, seq_lens, out, plan->err, B, Hq, Hkv,
+                max_blocks, num_blocks, max_seq_len, nq, scale_log2, window, sinks,
+                out_dtype == PA_BF16, block_size, plan->num_sms, static_cast<char*>(plan->ws) + 64,
+                stream);
+            if (plan->ev_stop) cudaEventRecord(plan->ev_stop, stream);
+            plan->last_path = PA_PATH_PREFILL;
+            plan->last_blocks = 0;
+            plan->last_warps = 0;
+            return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+        }
         const int splits = pa::prefill_split_count(B, Hq, Hkv, nqq, vis_len, plan->num_sms);
         float* part = nullptr;
         if (splits > 1) {
@@ -510,11 +537,17 @@ pa_status decode_impl(const void* q, const int32_t* q_start, int T, int nq, cons
             plan->cnt_clean = std::min(plan->cnt_clean, plan->ws_bytes - need);
         }
         if (plan->ev_start) cudaEventRecord(plan->ev_start, stream);
-        const cudaError_t e = pa::launch_prefill(kmap, vmap, q, T, q_start, block_tables, seq_lens,
-                                                 out, plan->err, B, Hq, Hkv, max_blocks,
-                                                 num_blocks, max_seq_len, nq, scale_log2,
-                                                 out_dtype == PA_BF16, block_size, stream, part,
-                                                 splits, /*zero_invalid=*/1, window, sinks);
+        const cudaError_t e =
+            window > 0
+                ? pa::launch_prefill_one_tile(kmap, vmap, q, T, q_start, block_tables, seq_lens, out,
+                                              plan->err, B, Hq, Hkv, max_blocks, num_blocks, max_seq_len,
+                                              nq, scale_log2, out_dtype == PA_BF16, block_size, stream,
+                                              part, splits, /*zero_invalid=*/1, window, sinks)
+                : pa::launch_prefill(kmap, vmap, q, T, q_start, block_tables, seq_lens,
+                                     out, plan->err, B, Hq, Hkv, max_blocks,
+                                     num_blocks, max_seq_len, nq, scale_log2,
+                                     out_dtype == PA_BF16, block_size, stream, part,
+                                     splits, /*zero_invalid=*/1);
         if (plan->ev_stop) cudaEventRecord(plan->ev_stop, stream);
         plan->last_path = PA_PATH_PREFILL;
         plan->last_blocks = 0;

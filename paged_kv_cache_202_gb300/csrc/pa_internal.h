@@ -261,15 +261,15 @@ bool encode_query_map(CUtensorMap* map, const void* q, int T, int Hq, int g, int
 // run the one-tile kernel (pa_prefill_1t.cu), the others the two-tile
 // kernel. splits > 1 (one-tile kernel only) cuts every tile's key range into
 // that many blocks whose partials go to part (prefill_split_bytes) and are
-// merged by a second kernel. window > 0: a query at position p sees the tokens
-// t <= p with p - t < window or t < sinks (see WindowView).
+// merged by a second kernel.
 cudaError_t launch_prefill(const CUtensorMap& kmap, const CUtensorMap& vmap, const void* q,
                            int num_q, const int32_t* q_start, const int32_t* tables,
                            const int32_t* seq_lens, void* out, int* err, int B, int Hq, int Hkv,
                            int max_blocks, int num_blocks, int max_seq_len, int max_q,
                            float scale_log2, int out_bf16, int block_size, cudaStream_t stream,
-                           float* part = nullptr, int splits = 1, int zero_invalid = 0,
-                           int window = 0, int sinks = 0);
+                           float* part = nullptr, int splits = 1, int zero_invalid = 0);
+// window > 0: a query at position p sees the tokens t <= p with p - t < window
+// or t < sinks (see WindowView).
 cudaError_t launch_prefill_one_tile(const CUtensorMap& kmap, const CUtensorMap& vmap, const void* q,
                                     int num_q, const int32_t* q_start, const int32_t* tables,
                                     const int32_t* seq_lens, void* out, int* err, int B, int Hq,
@@ -277,6 +277,15 @@ cudaError_t launch_prefill_one_tile(const CUtensorMap& kmap, const CUtensorMap& 
                                     int max_q, float scale_log2, int out_bf16, int block_size,
                                     cudaStream_t stream, float* part, int splits,
                                     int zero_invalid, int window, int sinks);
+// The windowed call over many tiles: a list of items (ws, prefill_window_bytes
+// of it) and a persistent kernel over them; see pa_prefill_window.cu.
+cudaError_t launch_prefill_window(const CUtensorMap& kmap, const CUtensorMap& vmap, const void* q,
+                                  int num_q, const int32_t* q_start, const int32_t* tables,
+                                  const int32_t* seq_lens, void* out, int* err, int B, int Hq, int Hkv,
+                                  int max_blocks, int num_blocks, int max_seq_len, int max_q,
+                                  float scale_log2, int window, int sinks, int out_bf16, int block_size,
+                                  int num_sms, void* ws, cudaStream_t stream);
+size_t prefill_window_bytes(int B, int Hq, int Hkv, int num_q);
 // Key splits for a one-tile call (1: none) and the partial bytes they need;
 // nq = min(max_q, num_queries).
 int prefill_split_count(int B, int Hq, int Hkv, int64_t nq, int max_seq_len, int num_sms);

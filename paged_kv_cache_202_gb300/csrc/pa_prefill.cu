@@ -58,7 +58,6 @@
 #include <cuda_bf16.h>
 
 #include <algorithm>
-#include <type_traits>
 
 #include "pa.h"
 #include "pa_internal.h"
@@ -134,12 +133,6 @@ struct PrefillArgs {
     int probe_wait;           // 1: the MMA thread's first wait expires (a test hook)
     int max_q;                // bound on every sequence's query count
     int zero_invalid;         // 1: an invalid sequence's rows get zeros (multi-query calls)
-};
-
-// The window kernels' parameter: a longer one changes how the plain kernels
-// come out of the compiler (the one-tile kernel spilled).
-struct WindowPrefillArgs : PrefillArgs {
-    int window, sinks;
 };
 
 __device__ __forceinline__ void st_shared_v4(uint32_t addr, uint4 v) {
@@ -228,17 +221,11 @@ __device__ __forceinline__ bool wait_role(uint32_t bar, uint32_t parity, volatil
     }
 }
 
-template <bool WIN>
-using KernelArgs = std::conditional_t<WIN, WindowPrefillArgs, PrefillArgs>;
-
-// WIN: sliding window with sinks. The block's chunks run over the visible
-// indices of its rows (WindowView): token limits, pages and masks below count
-// those, and `skip` maps a page to its logical one.
-template <int BS, bool WIN>
+template <int BS>
 __global__ void __launch_bounds__(kThreads, 1)
     prefill_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                    const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap omap,
-                   const KernelArgs<WIN> a) {
+                   const PrefillArgs a) {
     extern __shared__ uint8_t smem_raw[];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t raw = smem_addr(smem_raw);
@@ -272,7 +259,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int limit = min(a.max_seq_len, a.max_blocks * BS);
     {
         const int64_t qs64 = a.q_start[b], n64 = static_cast<int64_t>(a.q_start[b + 1]) - qs64;
-        if (WIN && n64 == 0) return;  // a request without queries in this step
         if (n64 < 1 || n64 > a.max_q || L < n64 || L > limit || qs64 < 0 || qs64 + n64 > a.num_q) {
             if (blockIdx.x == 0 && h == 0 && tid == 0) atomicOr(a.err, kErrSeqLen);
             // The rows inside the arrays get zeros in a multi-query call and
@@ -290,16 +276,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int nq0 = min(a.Qb, n - q0);
     const int nq1 = max(0, min(a.Qb, n - q0 - a.Qb));
     const bool two = nq1 > 0;
-    const int end = L - n + q0 + (two ? a.Qb + nq1 : nq0);  // tokens up to the last row
-    int window = 0, sinks = 0;
-    WindowView view{0, 0, 0};
-    if constexpr (WIN) {
-        window = a.window;
-        sinks = a.sinks;
-        view = window_view(L - n + q0, end - 1, window, sinks, BS);
-    }
-    const int ntok = WIN ? view.len : end;  // tokens (visible indices) the last row sees
-    auto logical = [&](int p) { return WIN && p >= (sinks + BS - 1) / BS ? p + view.skip : p; };
+    const int ntok = L - n + q0 + (two ? a.Qb + nq1 : nq0);  // tokens the last row sees
     const int nc = (ntok + kChunk - 1) / kChunk;
     const int nb = (ntok + BS - 1) / BS;
     const int32_t* table = a.tables + static_cast<size_t>(b) * a.max_blocks;
@@ -342,7 +319,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // The table entries this block reads, validated once.
     bool bad = false;
     for (int i = tid; i < nb; i += kThreads) {
-        const int p = table[logical(i)];
+        const int p = table[i];
         bad |= p < 0 || p >= a.num_blocks;
     }
     if (__syncthreads_or(bad)) {
@@ -400,7 +377,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int j = 0; j < kPages; ++j) {
                     const int p = c * kPages + j;
-                    pg[j] = p < nb ? table[logical(p)] : 0;
+                    pg[j] = p < nb ? table[p] : 0;
                 }
             };
             load_pages(0);
@@ -525,8 +502,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t lane_base = static_cast<uint32_t>(32 * quarter + 16 * sub16) << 16;
         const uint32_t s_addr = tmem + lane_base + col_s(t);
         const uint32_t o_addr = tmem + lane_base + col_o(t);
-        const int pos_r = L - n + q0 + t * a.Qb + qi - (WIN ? view.skip * BS : 0);  // last token (index) this row sees
-        const int lo_r = WIN ? pos_r - window : -1;  // from sinks to here: hidden from it
+        const int pos_r = L - n + q0 + t * a.Qb + qi;  // last token this row sees
         float m = -INFINITY, l = 0.f;
         bool ok = true;
         for (int c = 0; c < nc; ++c) {
@@ -540,14 +516,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc::wait_ld();
             // Causal mask by predicate; the warp skips it when no row needs it.
             const int tok0 = c * kChunk + 64 * half;
-            const bool all_seen = c * kChunk + kChunk - 1 <= pos_r &&
-                                  (!WIN || c * kChunk > lo_r || c * kChunk + kChunk <= sinks);
-            if (!__all_sync(0xffffffffu, row_valid && all_seen)) {
+            if (!__all_sync(0xffffffffu, row_valid && c * kChunk + kChunk - 1 <= pos_r)) {
 #pragma unroll
-                for (int i = 0; i < kChunk / 2; ++i) {
-                    const bool seen = tok0 + i <= pos_r && (!WIN || tok0 + i > lo_r || tok0 + i < sinks);
-                    sv[i] = (row_valid && seen) ? sv[i] : -INFINITY;
-                }
+                for (int i = 0; i < kChunk / 2; ++i)
+                    sv[i] = (row_valid && tok0 + i <= pos_r) ? sv[i] : -INFINITY;
             }
             // Row max: three-input max over pairs, four short chains, then the
             // partner's half.
@@ -600,14 +572,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             // Final chunk: tile 0 zeroes the V rows past the last token (both
             // tiles' products run after tile 0 has published its P).
-            // With a window, also the rows between the sinks and the first
-            // row's window, which no row sees. (S_0(c) was issued after
-            // PV_0(c - 1), which waited for V(c - 1), so no earlier phase of
-            // the stage is open and this parity wait is unambiguous.)
-            const int h0 = WIN ? max(0, sinks - c * kChunk) : 0;
-            const int h1 = WIN ? min(kChunk, view.lo - c * kChunk) : 0;
-            if (t == 0 && (c == nc - 1 || h0 < h1)) {
-                const int valid = WIN ? min(kChunk, ntok - c * kChunk) : ntok - c * kChunk;
+            if (t == 0 && c == nc - 1) {
+                const int valid = ntok - c * kChunk;
                 // V of this chunk arrives on its own barrier.
                 ok = __all_sync(0xffffffffu, wait_role(bars + kBarVFull + 8 * (c % kStagesV),
                                                        (c / kStagesV) & 1, abort_flag, a.err));
@@ -616,13 +582,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const uint32_t vst = base + kOffV + (c % kStagesV) * kStageKV;
                     for (int idx = tid; idx < (kChunk - valid) * 16; idx += kTileThreads) {
                         const int r = valid + (idx >> 4), hf = (idx >> 3) & 1, ch = idx & 7;
-                        st_shared_v4(vst + hf * kHalfKV + r * 128 + ch * 16, make_uint4(0, 0, 0, 0));
-                    }
-                }
-                if constexpr (WIN) {
-                    const uint32_t vst = base + kOffV + (c % kStagesV) * kStageKV;
-                    for (int idx = tid; idx < (h1 - h0) * 16; idx += kTileThreads) {
-                        const int r = h0 + (idx >> 4), hf = (idx >> 3) & 1, ch = idx & 7;
                         st_shared_v4(vst + hf * kHalfKV + r * 128 + ch * 16, make_uint4(0, 0, 0, 0));
                     }
                 }
@@ -694,7 +653,7 @@ cudaError_t launch_prefill(const CUtensorMap& kmap, const CUtensorMap& vmap, con
                            const int32_t* seq_lens, void* out, int* err, int B, int Hq, int Hkv,
                            int max_blocks, int num_blocks, int max_seq_len, int max_q,
                            float scale_log2, int out_bf16, int block_size, cudaStream_t stream,
-                           float* part, int splits, int zero_invalid, int window, int sinks) {
+                           float* part, int splits, int zero_invalid) {
     // The one-tile kernel overlaps a tile's softmax with its own next score
     // products (~2,100 cycles per 128-token chunk and tile); this kernel
     // alternates two tiles (~3,100 cycles per chunk for both), which halves
@@ -719,11 +678,9 @@ cudaError_t launch_prefill(const CUtensorMap& kmap, const CUtensorMap& vmap, con
             return launch_prefill_one_tile(kmap, vmap, q, num_q, q_start, tables, seq_lens, out, err,
                                            B, Hq, Hkv, max_blocks, num_blocks, max_seq_len, max_q,
                                            scale_log2, out_bf16, block_size, stream, part,
-                                           splits, zero_invalid, window, sinks);
+                                           splits, zero_invalid, 0, 0);
     }
-    WindowPrefillArgs a{};
-    a.window = window;
-    a.sinks = sinks;
+    PrefillArgs a{};
     a.q = static_cast<const uint16_t*>(q);
     a.q_start = q_start;
     a.tables = tables;
@@ -756,18 +713,13 @@ cudaError_t launch_prefill(const CUtensorMap& kmap, const CUtensorMap& vmap, con
     } else {
         omap = qmap;  // not used: float output is written by the threads
     }
-    auto launch = [&](auto kern, const auto& args) {
-        const cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void*>(kern),
-                                                   cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                   static_cast<int>(kSmemBytes));
-        if (e != cudaSuccess) return e;
-        kern<<<grid, kThreads, kSmemBytes, stream>>>(kmap, vmap, qmap, omap, args);
-        return cudaGetLastError();
-    };
-    if (window > 0)
-        return launch(block_size == 16 ? prefill_kernel<16, true> : prefill_kernel<32, true>, a);
-    return launch(block_size == 16 ? prefill_kernel<16, false> : prefill_kernel<32, false>,
-                  static_cast<const PrefillArgs&>(a));
+    auto kern = block_size == 16 ? prefill_kernel<16> : prefill_kernel<32>;
+    cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void*>(kern),
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         static_cast<int>(kSmemBytes));
+    if (e != cudaSuccess) return e;
+    kern<<<grid, kThreads, kSmemBytes, stream>>>(kmap, vmap, qmap, omap, a);
+    return cudaGetLastError();
 }
 
 }  // namespace pa

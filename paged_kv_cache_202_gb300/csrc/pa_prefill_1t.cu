@@ -522,7 +522,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t lane_base = static_cast<uint32_t>(32 * quarter + 16 * sub16) << 16;
         const uint32_t o_addr = tmem + lane_base + kColO;
         const int pos_r = L - n + q0 + qi - (WIN ? view.skip * BS : 0);  // last token (index) this row sees
-        const int lo_r = WIN ? pos_r - window : -1;   // from sinks to here: hidden from it
         float* mpub = reinterpret_cast<float*>(gbase + kOffM);
         float m_l = -INFINITY, l = 0.f;  // this thread's part of the row sum, in units of 2^m_l
         bool ok = true;
@@ -539,12 +538,27 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc::wait_ld();
             // Causal mask by predicate; the warp skips it when no row needs it.
             const int tok0 = c * kChunk + 64 * half;
-            if (!__all_sync(0xffffffffu, row_valid && c * kChunk + kChunk - 1 <= pos_r &&
-                                             (!WIN || c * kChunk > lo_r || c * kChunk + kChunk <= sinks))) {
+            if constexpr (!WIN) {
+                if (!__all_sync(0xffffffffu, row_valid && c * kChunk + kChunk - 1 <= pos_r)) {
 #pragma unroll
-                for (int i = 0; i < kChunk / 2; ++i)
-                    sv[i] = (row_valid && tok0 + i <= pos_r &&
-                             (!WIN || tok0 + i > lo_r || tok0 + i < sinks)) ? sv[i] : -INFINITY;
+                    for (int i = 0; i < kChunk / 2; ++i)
+                        sv[i] = (row_valid && tok0 + i <= pos_r) ? sv[i] : -INFINITY;
+                }
+            } else {
+                // Each end of the window by itself: most chunks have neither.
+                // Rows past the tile's queries are never stored, so they need
+                // no mask.
+                if (__any_sync(0xffffffffu, row_valid && c * kChunk + kChunk - 1 > pos_r)) {
+                    const int last = pos_r - tok0;
+#pragma unroll
+                    for (int i = 0; i < kChunk / 2; ++i) sv[i] = i <= last ? sv[i] : -INFINITY;
+                }
+                const int lo_r = pos_r - a.window;  // from the sinks to here: hidden from this row
+                if (__any_sync(0xffffffffu, row_valid && c * kChunk <= lo_r && c * kChunk + kChunk > a.sinks)) {
+                    const int h0 = a.sinks - tok0, h1 = lo_r - tok0;
+#pragma unroll
+                    for (int i = 0; i < kChunk / 2; ++i) sv[i] = (i < h0 || i > h1) ? sv[i] : -INFINITY;
+                }
             }
             // Row max: three-input max over pairs, four short chains, then the
             // partner's half.
