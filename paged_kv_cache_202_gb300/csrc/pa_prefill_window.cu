@@ -73,7 +73,6 @@ constexpr uint32_t kTmemCols = 512;
 __host__ __device__ constexpr uint32_t col_s(int t) { return 128u * t; }
 __host__ __device__ constexpr uint32_t col_o(int t) { return 256u + 128u * t; }
 constexpr float kRescaleLog2 = 8.f;
-constexpr int kHandOver = 7;  // score pair of P's second part at which the first is handed over
 
 // Shared-memory layout (byte offsets from a 1024-aligned base).
 constexpr uint32_t kTileQ = 32768;                    // 2 halves x 128 rows x 128 B
@@ -89,8 +88,8 @@ constexpr uint32_t kBarKEmpty = kBarKFull + 8 * kStagesK;
 constexpr uint32_t kBarVFull = kBarKEmpty + 8 * kStagesK;  // [kStagesV]
 constexpr uint32_t kBarVEmpty = kBarVFull + 8 * kStagesV;
 constexpr uint32_t kBarS = kBarVEmpty + 8 * kStagesV;      // [tile] scores ready
-constexpr uint32_t kBarP = kBarS + 16;                     // [tile][part] P stored, kTileThreads arrivals
-constexpr uint32_t kBarO = kBarP + 32;                     // [tile] an item's last value product done
+constexpr uint32_t kBarP = kBarS + 16;                     // [tile] P stored, kTileThreads arrivals
+constexpr uint32_t kBarO = kBarP + 16;                     // [tile] an item's last value product done
 constexpr uint32_t kBarQFull = kBarO + 16;                 // [tile] queries landed
 constexpr uint32_t kBarQEmpty = kBarQFull + 16;            // [tile] an item's last score product done
 constexpr uint32_t kBarDrain = kBarQEmpty + 16;
@@ -351,9 +350,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         for (int u = 0; u < 2; ++u) {
             mbar_init(bars + kBarS + 8 * u, 1);
-            // Tile 0's first part also waits for the warp that zeroes value rows.
-            mbar_init(bars + kBarP + 16 * u, kTileThreads + (u == 0 ? 1 : 0));
-            mbar_init(bars + kBarP + 16 * u + 8, kTileThreads);
+            // Tile 0's also waits for the warp that zeroes value rows.
+            mbar_init(bars + kBarP + 8 * u, kTileThreads + (u == 0 ? 1 : 0));
             mbar_init(bars + kBarO + 8 * u, 1);
             mbar_init(bars + kBarQFull + 8 * u, 1);
             mbar_init(bars + kBarQEmpty + 8 * u, 1);
@@ -482,16 +480,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 tc::commit_if(one, bars + kBarS + 8 * u);
             };
-            // O_u (+)= P_u V of the chunk in V stage s, in the two parts that the
-            // softmax hands over: tokens 0-31 and 64-95, then the others.
-            auto issue_pv = [&](int u, int part, int s, uint32_t add) {
+            // O_u (+)= P_u V of the chunk in V stage s.
+            auto issue_pv = [&](int u, int s, uint32_t add) {
                 const uint32_t b0 = lo_v + s * (kStageKV >> 4);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {              // 16 tokens = 8 columns of P
-                    const int kk = (i >> 1) * 4 + part * 2 + (i & 1);
+                for (int kk = 0; kk < kChunk / 16; ++kk)   // 16 tokens = 8 columns of P
                     tc::mma_bf16_ts_if(one, tm + col_o(u), tm + col_s(u) + kk * 8, b0 + kk * (2048 >> 4), hi,
-                                       kIdescO, i > 0 || part > 0 ? 1u : add);
-                }
+                                       kIdescO, kk > 0 ? 1u : add);
             };
             bool ok = true;
             if (a.probe_wait) {
@@ -515,11 +510,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 two = __shfl_sync(0xffffffffu, more && w.it.nq > a.Qb ? 1 : 0, 0);
             };
             auto value_products = [&](int u, uint32_t add) {
-                if (!wait(kBarP + 16 * u, pp[u])) return false;
-                issue_pv(u, 0, vs, add);
-                if (!wait(kBarP + 16 * u + 8, pp[u])) return false;
-                issue_pv(u, 1, vs, add);
+                if (!wait(kBarP + 8 * u, pp[u])) return false;
                 pp[u] ^= 1u;
+                issue_pv(u, vs, add);
                 return true;
             };
             auto query_tile = [&](int u) {       // an item's first score product of tile u
@@ -549,11 +542,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const bool more = nc > 0;
                     // The last score products of their item free its queries.
                     const bool last = end ? nc == 1 : c + 2 == n;
-                    ok = wait(kBarVFull + 8 * vs, vp) && value_products(0, c > 0);
+                    // What the products need besides P is there by now; P comes
+                    // last, so that nothing is waited for between them.
+                    ok = wait(kBarVFull + 8 * vs, vp) && (!more || wait(kBarKFull + 8 * ks, kp)) &&
+                         value_products(0, c > 0);
                     if (!ok) break;
                     if (end) tc::commit_if(one, bars + kBarO);
                     if (more) {
-                        ok = (!end || query_tile(0)) && wait(kBarKFull + 8 * ks, kp);
+                        ok = !end || query_tile(0);
                         if (!ok) break;
                         issue_s(0, ks);
                         if (last) tc::commit_if(one, bars + kBarQEmpty);
@@ -697,9 +693,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const float m_use = m == -INFINITY ? 0.f : m;
                 const uint64_t sc2 = f32x2(a.scale_log2, a.scale_log2), nm2 = f32x2(-m_use, -m_use);
                 uint64_t ps2[2] = {f32x2(0.f, 0.f), f32x2(0.f, 0.f)};
-                // P in two parts of 32 scores a thread. The first is handed over
-                // half way through the second, when its store has completed, so
-                // that its value products run meanwhile.
 #pragma unroll
                 for (int h2 = 0; h2 < 2; ++h2) {
                     uint32_t pw[16];
@@ -710,17 +703,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                         const float p0 = fast_exp2(x.x), p1 = fast_exp2(x.y);
                         ps2[i & 1] = add_f32x2(ps2[i & 1], f32x2(p0, p1));
                         pw[i] = pack_bf16x2(p0, p1);
-                        if (h2 == 1 && i == kHandOver) {
-                            tc::wait_st();
-                            tc::fence_before_sync();
-                            mbar_arrive(bars + kBarP + 16 * t);
-                        }
                     }
                     tc::st16x2_16u<32>(s_addr + 16 * h2, pw);
                 }
                 tc::wait_st();
                 tc::fence_before_sync();
-                mbar_arrive(bars + kBarP + 16 * t + 8);
+                mbar_arrive(bars + kBarP + 8 * t);
                 const float2 s0 = f32x2_split(ps2[0]), s1 = f32x2_split(ps2[1]);
                 l += (s0.x + s0.y) + (s1.x + s1.y);
             }
