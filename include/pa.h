@@ -660,15 +660,18 @@ pa_status pa_qk_rope_append(const void* q, int64_t q_stride, const void* k, int6
  *
  *   window    >= 1;  sinks >= 0 (0: a plain sliding window)
  *   other arguments, limits and device errors as for pa_decode, bf16 pools only
- *   (PA_ERR_DTYPE); the plan's forced path does not apply, PA_MERGE_FUSED is
- *   refused (PA_ERR_SHAPE). seq_lens are the full lengths.
+ *   (PA_ERR_DTYPE); the plan's forced path, merge and schedule do not apply.
+ *   seq_lens are the full lengths.
  *
- * Cost: the bytes of min(L_b, window + sinks) tokens rounded to pages. Calls
- * on one plan must be ordered on the device (one stream, or events): they
- * share its workspace. A call that needs a larger workspace during a stream
- * capture returns PA_ERR_WORKSPACE: make the call once before capturing it.
- * Memory that this call and pa_prefill_window outgrow is kept until pa_free,
- * so graphs captured with the plan stay valid.
+ * Cost: the bytes of min(L_b, window + sinks) tokens rounded to pages. A
+ * sequence's pages are divided among the warps of one block or cluster, whose
+ * results are merged on the chip; a few sequences with very long windows run on
+ * pa_decode's split kernels and the plan's workspace. Calls on one plan must be
+ * ordered on the device (one stream, or events). A call that has to create the
+ * plan or needs a larger workspace during a stream capture returns
+ * PA_ERR_WORKSPACE: make the call once before capturing it. Memory that this
+ * call and pa_prefill_window outgrow is kept until pa_free, so graphs captured
+ * with the plan stay valid.
  */
 pa_status pa_decode_window(const void* q, const void* k_pool, const void* v_pool,
                            const int32_t* block_tables, int max_blocks, const int32_t* seq_lens,

@@ -311,6 +311,7 @@ struct pa_plan {
     MapKey kkey, vkey;
     CUtensorMap kmap, vmap;
     std::vector<OccKey> occ;
+    std::vector<pa::WindowRoom> rooms;
 };
 
 extern "C" {
@@ -381,14 +382,18 @@ pa_status grow_workspace(pa_plan* plan, size_t need, cudaStream_t stream) {
     return PA_OK;
 }
 
-// Which kernel a windowed multi-query call runs: the persistent one over pairs
-// of tiles, or (few tiles, or one tile a sequence) the one-tile kernel with its
-// key split.
+// Which kernel a windowed multi-query call runs: the one-tile kernel where every
+// sequence fits one tile (the other's second tile would be empty: 64 sequences
+// of 40 queries, one head a group, W = 4096: 194 against 221 us) or where its
+// tiles do not fill the SMs once, so that its key split can (512 queries, 128
+// tiles, W = 1024: 19 against 27 us); the persistent kernel over pairs of tiles
+// otherwise (1024 queries, 256 tiles: 28 against 36 us; 16 x 256 queries, 1024
+// tiles, W = 2048: 143 against 184 us).
 bool window_items(int B, int Hq, int Hkv, int64_t nq, int num_sms) {
     const int qb = 128 / (Hq / Hkv);
     const int force = pa::prefill_kernel_choice();  // a test may pin either kernel
     if (force != PA_PREFILL_AUTO) return force == PA_PREFILL_TWO_TILE;
-    return nq > qb && (nq + qb - 1) / qb * static_cast<int64_t>(Hkv) * B > 3LL * num_sms;
+    return nq > qb && (nq + qb - 1) / qb * static_cast<int64_t>(Hkv) * B > num_sms;
 }
 
 // The decode of pa_decode, with q_start != null (T query rows, at most nq per
@@ -555,6 +560,50 @@ pa_status decode_impl(const void* q, const int32_t* q_start, int T, int nq, cons
         return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
     }
 
+    // The pools' tensor maps, kept in the plan while the pools are the same.
+    auto pool_maps = [&]() -> bool {
+        const int rows = num_blocks * Hkv;
+        MapKey kk{k_pool, rows, D, block_size}, vk{v_pool, rows, D, block_size};
+        if (!(plan->kkey == kk)) {
+            plan->kkey = MapKey{};
+            if (!pa::encode_pool_map(&plan->kmap, k_pool, rows, D, block_size)) return false;
+            plan->kkey = kk;
+        }
+        if (!(plan->vkey == vk)) {
+            plan->vkey = MapKey{};
+            if (!pa::encode_pool_map(&plan->vmap, v_pool, rows, D, block_size)) return false;
+            plan->vkey = vk;
+        }
+        return true;
+    };
+    if (window > 0) {
+        // One block or cluster per segment, merged on the chip, or, where the
+        // segments are so few and so long that they would leave half of the
+        // SMs without work for more than eight rounds, the split kernels over
+        // one page stream. Measured, us: one sequence, one kv head, W = 8191:
+        // 12.9 against 13.7 split, W = 32768: 27.7 against 17.4, W = 65536:
+        // 46.4 against 22.3; 8 segments, W = 8191: 12.1 against 18.6, W = 32768:
+        // 32.4 against 33.1, W = 65536: 55.9 against 52.8.
+        pa::WindowDecodeShape shape;
+        if (pa::window_decode_shape(static_cast<int64_t>(B) * sh.U, sh.GS, D, block_size, vis_len, plan->num_sms,
+                                    &plan->rooms, &shape) != cudaSuccess)
+            return PA_ERR_CUDA;
+        if (2 * shape.at_work >= 12LL * plan->num_sms || shape.rounds <= 8) {
+            if (!pool_maps()) return PA_ERR_CUDA;
+            if (plan->ev_start) cudaEventRecord(plan->ev_start, stream);
+            const cudaError_t e = pa::launch_window_decode(
+                plan->kmap, plan->vmap, q, block_tables, seq_lens, out, plan->err, B, Hq, Hkv, D, block_size,
+                max_blocks, num_blocks, max_seq_len, scale_log2, window, sinks, out_dtype == PA_BF16, sh.nslices,
+                sh.GS, shape, stream);
+            if (plan->ev_stop) cudaEventRecord(plan->ev_stop, stream);
+            plan->last_path = PA_PATH_MMA;
+            plan->last_blocks = static_cast<int>(static_cast<int64_t>(B) * sh.U * shape.cluster);
+            plan->last_warps = static_cast<int>(std::min<int64_t>(
+                static_cast<int64_t>(plan->last_blocks) * shape.warps, INT32_MAX));
+            return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+        }
+    }
+
     // The append as its own kernel, for the paths that do not fuse it: the
     // step's rows at position seq_lens[b] - 1, before the decode reads them.
     auto append_first = [&]() -> cudaError_t {
@@ -586,7 +635,7 @@ pa_status decode_impl(const void* q, const int32_t* q_start, int T, int nq, cons
     L.win = window > 0 ? 1 : 0;
     const bool can_fuse = !L.win && !q_start && sh.kind == pa::kSplitMma && sh.NT == 1 && sh.warps == 3;
     L.fused = can_fuse && plan->merge_mode == PA_MERGE_FUSED ? 1 : 0;
-    if (plan->merge_mode == PA_MERGE_FUSED && !can_fuse) return PA_ERR_SHAPE;
+    if (plan->merge_mode == PA_MERGE_FUSED && !can_fuse && !L.win) return PA_ERR_SHAPE;
     // The append rides in the split kernel on the one-n-tile tensor-core
     // tiles (up to 8 query heads per kv head) with one stage per warp and the
     // merge kernel; elsewhere it runs first on its own. With two n-tiles the

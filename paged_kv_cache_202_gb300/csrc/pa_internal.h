@@ -5,6 +5,8 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <vector>
+
 namespace pa {
 
 // Workspace metadata written by block 0 of the split kernel and read by the
@@ -286,6 +288,26 @@ cudaError_t launch_prefill_window(const CUtensorMap& kmap, const CUtensorMap& vm
                                   float scale_log2, int window, int sinks, int out_bf16, int block_size,
                                   int num_sms, void* ws, cudaStream_t stream);
 size_t prefill_window_bytes(int B, int Hq, int Hkv, int num_q);
+// pa_decode_window's kernel (pa_window_decode.cu). The clusters of each size (1,
+// 2, 4, 8 blocks) that the device holds at a time with one, two or four blocks
+// an SM, kept in the plan; the warps per block and blocks per segment of a call.
+struct WindowRoom {
+    int D, BS, GS;
+    int room[3][4];
+};
+struct WindowDecodeShape {
+    int warps = 0, cluster = 0;
+    int64_t rounds = 0;    // chunks per warp
+    int64_t at_work = 0;   // warps of all segments
+};
+// segs = B x kv units; vis_len bounds the visible tokens of a sequence.
+cudaError_t window_decode_shape(int64_t segs, int GS, int D, int block_size, int vis_len, int num_sms,
+                                std::vector<WindowRoom>* rooms, WindowDecodeShape* out);
+cudaError_t launch_window_decode(const CUtensorMap& kmap, const CUtensorMap& vmap, const void* q,
+                                 const int32_t* tables, const int32_t* seq_lens, void* out, int* err, int B,
+                                 int Hq, int Hkv, int D, int block_size, int max_blocks, int num_blocks,
+                                 int max_seq_len, float scale_log2, int window, int sinks, int out_bf16,
+                                 int nslices, int GS, const WindowDecodeShape& shape, cudaStream_t stream);
 // Key splits for a one-tile call (1: none) and the partial bytes they need;
 // nq = min(max_q, num_queries).
 int prefill_split_count(int B, int Hq, int Hkv, int64_t nq, int max_seq_len, int num_sms);

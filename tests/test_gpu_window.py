@@ -165,6 +165,18 @@ def test_decode_wrong_lengths_and_entries():
     assert bool((out[[1, 3]] == 0).all()) and torch.equal(out[[0, 2]], good[[0, 2]])
 
 
+def test_a_wrong_entry_anywhere_zeroes_its_rows():
+    c = Case([900, 900, 40], Hq=8, Hkv=4, W=800, S=4, seed=5).upload()
+    good = c.run()
+    c.check(good)
+    for page in (0, 7, 30, 56):
+        c.upload()
+        c.d["table"][1, page] = -3
+        out = c.run()
+        assert pa.pa_last_device_error(c.plan) == pa.PA_DEVERR_TABLE
+        assert bool((out[1] == 0).all()) and torch.equal(out[[0, 2]], good[[0, 2]])
+
+
 def test_rows_behind_are_left_alone():
     c = Case([70, 9, 200], W=30, S=2).upload()
     big = torch.full((5, 8, 128), 7.5, dtype=torch.bfloat16, device="cuda")
@@ -174,16 +186,33 @@ def test_rows_behind_are_left_alone():
     c.check(big[1:4])
 
 
-def test_decode_refuses_forms_it_has_not():
+def test_forced_paths_and_merges_do_not_apply():
     c = Case([70, 9], W=30, S=2).upload()
     c.run()
     c.plan.set_merge(pa.PA_MERGE_FUSED)
-    with pytest.raises(pa.PagedAttentionError) as e:
-        c.run()
-    assert e.value.status == pa.PA_ERR_SHAPE
-    c.plan.set_merge(pa.PA_MERGE_AUTO)
-    c.plan.set_path(pa.PA_PATH_SIMPLE)       # does not apply
+    c.plan.set_path(pa.PA_PATH_SIMPLE)
     c.check(c.run())
+
+
+@pytest.mark.parametrize("lens,Hq,Hkv,W,bs", [
+    ([40000], 8, 1, 33000, 16), ([21000, 40000], 4, 1, 20000, 32), ([30000], 12, 1, 29000, 16), ([30000], 34, 2, 29000, 16),
+])
+def test_decode_of_few_long_segments(lens, Hq, Hkv, W, bs):
+    c = Case(lens, Hq=Hq, Hkv=Hkv, W=W, S=19, bs=bs, seed=Hq).upload()
+    c.check(c.run())
+
+
+@pytest.mark.parametrize("D,bs", [(64, 16), (128, 16), (128, 32)])
+@pytest.mark.parametrize("Hq,Hkv", [(4, 1), (16, 1), (8, 4), (32, 32)])
+@pytest.mark.parametrize("B", [1, 2, 5, 9, 17, 40, 130])
+def test_decode_cluster_shapes(B, Hq, Hkv, D, bs):
+    # From one segment to more than the device holds blocks at a time: every
+    # cluster size and number of warps, with sequences that leave some blocks of
+    # a cluster, and some warps of a block, without a chunk.
+    rng = np.random.default_rng(B + Hq)
+    lens = rng.integers(1, 900, size=B).tolist()
+    c = Case(lens, Hq=Hq, Hkv=Hkv, D=D, bs=bs, W=600, S=7, seed=B).upload()
+    c.check(c.run(), rows=set(range(0, B, max(1, B // 12))))
 
 
 KERNELS = [pa.PA_PREFILL_AUTO, pa.PA_PREFILL_ONE_TILE, pa.PA_PREFILL_TWO_TILE]
