@@ -152,6 +152,7 @@ cudaError_t launch_split_window(const SplitLaunch& L, const CUtensorMap& kmap,
 constexpr size_t kSmemLimit = 232448;  // opt-in dynamic shared memory per block on sm_10x
 constexpr int kMaxBatch = 8192;        // per-sequence arrays live in shared memory
 constexpr int64_t kMaxRows = int64_t(1) << 30;  // output rows (rows x heads), counted in int
+constexpr int kSms = 152;              // of the GB300, for grids that need no plan
 constexpr int kMaxGridYZ = 65535;      // grid.y / grid.z limit of the prefill launch
 
 // Kv units, tile width and block shape, from the sizes alone.

@@ -19,12 +19,20 @@
 // (half layout) or whole pairs (interleaved), so that a rotation needs no
 // exchange and rows may be rotated in place. 8 threads hold a 128-element
 // bf16 head; a warp takes 4 heads at a time and goes over the heads of one
-// row, so a thread's 8 sines and cosines serve all its heads. The bytes bound
-// it: every element is read once and written once.
+// row, so a thread's 8 sines and cosines serve all its heads (few rows: several
+// warps share a row). The bytes bound it -- every element is read once and
+// written once: 16421 rows of 32 + 8 heads 51.9 us, 6.48 TB/s -- until the norms
+// come in, whose arithmetic fills 60 % of the issue slots: 32768 rows of 32 + 8 +
+// 8 heads 135 us, 5.96 TB/s (126 us without norms). Few rows are bound by the
+// launch and one round trip: 64 rows 2.4 us, 2.8 us with the cache write.
+// A ring of rows in shared memory filled by bulk copies, instead of loads held in
+// registers, measured 153 us for the 32768 rows and 61 us for 16384 rows without
+// norms.
 #include <algorithm>
 #include <atomic>
 #include <cmath>
 #include <cstdint>
+#include <type_traits>
 
 #include "pa.h"
 #include "pa_internal.h"
@@ -33,7 +41,7 @@
 namespace pa {
 namespace {
 
-constexpr int kRopeWarps = 4;  // warps a block
+constexpr int kRopeWarps = 4;   // warps a block
 
 struct RopeArgs {
     const void *q, *k, *v;          // rows: [T][H][D], row strides in elements
@@ -62,54 +70,80 @@ __device__ __forceinline__ float2 sin_cos(int pos, uint64_t turn) {
     return make_float2(quarter & 2 ? -s1 : s1, (quarter + 1) & 2 ? -c1 : c1);
 }
 
-template <typename T>
-struct Vec;
-template <>
-struct Vec<uint16_t> {
+// A thread's two 16-byte vectors of a head as the two ends of its N pairs, two
+// pairs to a 64-bit register for the paired arithmetic: with the half layout
+// one vector holds the first ends and the other the second, with the
+// interleaved one both hold whole pairs.
+template <typename T, bool HALF>
+struct Pairs;
+template <bool HALF>
+struct Pairs<uint16_t, HALF> {
     static constexpr int N = 8;
-    static __device__ __forceinline__ void unpack(uint4 w, float* x) {
-        const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+    static __device__ __forceinline__ void unpack(uint4 w0, uint4 w1, uint64_t (&x1)[4], uint64_t (&x2)[4]) {
+        const uint32_t u[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            x[2 * i] = bf16_lo(u[i]);
-            x[2 * i + 1] = bf16_hi(u[i]);
+            x1[i] = HALF ? f32x2(bf16_lo(u[i]), bf16_hi(u[i])) : f32x2(bf16_lo(u[2 * i]), bf16_lo(u[2 * i + 1]));
+            x2[i] = HALF ? f32x2(bf16_lo(u[i + 4]), bf16_hi(u[i + 4]))
+                         : f32x2(bf16_hi(u[2 * i]), bf16_hi(u[2 * i + 1]));
         }
     }
-    static __device__ __forceinline__ uint4 pack(const float* x) {
-        return make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]),
-                          pack_bf16x2(x[6], x[7]));
+    static __device__ __forceinline__ void pack(const uint64_t (&x1)[4], const uint64_t (&x2)[4], uint4& w0, uint4& w1) {
+        uint32_t u[8];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float2 a = f32x2_split(x1[i]), b = f32x2_split(x2[i]);
+            u[HALF ? i : 2 * i] = HALF ? pack_bf16x2(a.x, a.y) : pack_bf16x2(a.x, b.x);
+            u[HALF ? i + 4 : 2 * i + 1] = HALF ? pack_bf16x2(b.x, b.y) : pack_bf16x2(a.y, b.y);
+        }
+        w0 = make_uint4(u[0], u[1], u[2], u[3]);
+        w1 = make_uint4(u[4], u[5], u[6], u[7]);
     }
 };
-template <>
-struct Vec<float> {
+template <bool HALF>
+struct Pairs<float, HALF> {
     static constexpr int N = 4;
-    static __device__ __forceinline__ void unpack(uint4 w, float* x) {
-        x[0] = __uint_as_float(w.x);
-        x[1] = __uint_as_float(w.y);
-        x[2] = __uint_as_float(w.z);
-        x[3] = __uint_as_float(w.w);
+    static __device__ __forceinline__ void unpack(uint4 w0, uint4 w1, uint64_t (&x1)[2], uint64_t (&x2)[2]) {
+        const float f[8] = {__uint_as_float(w0.x), __uint_as_float(w0.y), __uint_as_float(w0.z),
+                            __uint_as_float(w0.w), __uint_as_float(w1.x), __uint_as_float(w1.y),
+                            __uint_as_float(w1.z), __uint_as_float(w1.w)};
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            x1[i] = HALF ? f32x2(f[2 * i], f[2 * i + 1]) : f32x2(f[4 * i], f[4 * i + 2]);
+            x2[i] = HALF ? f32x2(f[4 + 2 * i], f[5 + 2 * i]) : f32x2(f[4 * i + 1], f[4 * i + 3]);
+        }
     }
-    static __device__ __forceinline__ uint4 pack(const float* x) {
-        return make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]),
-                          __float_as_uint(x[3]));
+    static __device__ __forceinline__ void pack(const uint64_t (&x1)[2], const uint64_t (&x2)[2], uint4& w0, uint4& w1) {
+        float f[8];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const float2 a = f32x2_split(x1[i]), b = f32x2_split(x2[i]);
+            f[HALF ? 2 * i : 4 * i] = a.x;
+            f[HALF ? 2 * i + 1 : 4 * i + 2] = a.y;
+            f[HALF ? 4 + 2 * i : 4 * i + 1] = b.x;
+            f[HALF ? 5 + 2 * i : 4 * i + 3] = b.y;
+        }
+        w0 = make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
+        w1 = make_uint4(__float_as_uint(f[4]), __float_as_uint(f[5]), __float_as_uint(f[6]), __float_as_uint(f[7]));
     }
 };
 
-template <typename T, int D, bool HALF, bool APPEND>
-__global__ void __launch_bounds__(32 * kRopeWarps) rope_kernel(const __grid_constant__ RopeArgs a) {
-    constexpr int N = Vec<T>::N;      // elements a vector
+// BATCH: groups whose loads are in flight together; BLOCKS: blocks an SM holds at
+// least (a bound on registers); WHOLE: a group's heads are all queries or all keys.
+template <typename T, int D, bool HALF, bool APPEND, int BATCH, int BLOCKS, bool WHOLE>
+__global__ void __launch_bounds__(32 * kRopeWarps, BLOCKS) rope_kernel(const __grid_constant__ RopeArgs a) {
+    using P = Pairs<T, HALF>;
+    constexpr int N = P::N;           // elements a vector, pairs a thread
     constexpr int TPH = D / (2 * N);  // threads a head
-    constexpr int HPW = 32 / TPH;     // heads a warp takes at a time
+    constexpr int HPW = 32 / TPH;     // heads a warp takes at a time: a group
     griddep_wait();
     griddep_launch_dependents();
     const int lane = threadIdx.x & 31;
     const int64_t gw = static_cast<int64_t>(blockIdx.x) * kRopeWarps + (threadIdx.x >> 5);
-    const int t = static_cast<int>(gw / a.wpt);
+    const int t = a.wpt == 1 ? static_cast<int>(gw) : static_cast<int>(gw / a.wpt);
     if (t >= a.T) return;
-    const int g0 = static_cast<int>(gw - static_cast<int64_t>(t) * a.wpt) * a.gpw;
-    const int heads = a.Hq + (APPEND ? 2 : 1) * a.Hk;
-    const int groups = (heads + HPW - 1) / HPW;
-    const int g1 = min(g0 + a.gpw, groups);
+    const int g0 = a.wpt == 1 ? 0 : static_cast<int>(gw - static_cast<int64_t>(t) * a.wpt) * a.gpw;
+    const int g1 = g0 + a.gpw;  // this warp's groups: of the rotated heads, then of the values
     int64_t slot = 0;
     if constexpr (APPEND) {
         slot = a.slots[t];
@@ -119,6 +153,10 @@ __global__ void __launch_bounds__(32 * kRopeWarps) rope_kernel(const __grid_cons
         }
     }
     const int pos = a.positions[t];
+    const int64_t at = APPEND ? (((slot >> a.shift) * a.Hk << a.shift) + (slot & ((1 << a.shift) - 1))) * D
+                              : static_cast<int64_t>(t) * a.ko_stride;
+    const int kv_step = APPEND ? D << a.shift : D;  // from a head to the next of the keys' and values' outputs
+    const int rotated = (a.Hq + a.Hk + HPW - 1) / HPW;
     // This thread's two vectors of a head, and whether they are rotated.
     const int c = lane % TPH;
     int v0, v1;
@@ -134,103 +172,167 @@ __global__ void __launch_bounds__(32 * kRopeWarps) rope_kernel(const __grid_cons
         r0 = v0 * N < a.rot;
         r1 = v1 * N < a.rot;
     }
-    struct Group {       // this thread's part of a group of heads
-        uint4 w0, w1;
-        T* dst;
-        int kind;        // 0: q, 1: k, 2: v, 3: no head
-    };
-    auto load = [&](int g) {
-        const int head = g * HPW + lane / TPH;
-        Group r;
-        r.kind = head < a.Hq ? 0 : head < a.Hq + a.Hk ? 1 : head < heads ? 2 : 3;
-        const int h = head - (r.kind == 0 ? 0 : r.kind == 1 ? a.Hq : a.Hq + a.Hk);
-        r.w0 = r.w1 = make_uint4(0, 0, 0, 0);
-        r.dst = nullptr;
-        if (r.kind < 3) {
-            const T* src = static_cast<const T*>(r.kind == 0 ? a.q : r.kind == 1 ? a.k : a.v) +
-                           static_cast<int64_t>(t) * (r.kind == 0 ? a.q_stride : r.kind == 1 ? a.k_stride : a.v_stride) +
-                           h * D;
-            r.w0 = *reinterpret_cast<const uint4*>(src + v0 * N);
-            r.w1 = *reinterpret_cast<const uint4*>(src + v1 * N);
-            if (r.kind == 0) {
-                r.dst = static_cast<T*>(a.q_out) + static_cast<int64_t>(t) * a.qo_stride + h * D;
-            } else if constexpr (APPEND) {
-                r.dst = static_cast<T*>(r.kind == 1 ? a.kpool : a.vpool) +
-                        ((((slot >> a.shift) * a.Hk + h) << a.shift) + (slot & ((1 << a.shift) - 1))) * D;
-            } else {
-                r.dst = static_cast<T*>(a.k_out) + static_cast<int64_t>(t) * a.ko_stride + h * D;
+    uint64_t sn[N / 2], cs[N / 2];  // sines and cosines of this thread's pairs, two a register
+    bool have_angles = false;
+    // Groups f .. l - 1 of H heads: kind(h) tells the keys' heads from the queries',
+    // src(h) and dst(h) where a head's elements come from and go to.
+    auto turn = [&](auto is_key, auto src, auto dst, int H, int f, int l) {
+        uint4 q0 = make_uint4(0, 0, 0, 0), q1 = q0;  // this thread's weights of the kind at hand
+        int weight_kind = -1;
+        for (int g = f; g < l; g += BATCH) {
+            // Every load of the batch before any use.
+            uint4 w0[BATCH], w1[BATCH];
+#pragma unroll
+            for (int j = 0; j < BATCH; ++j) {
+                const int h = (g + j) * HPW + lane / TPH;
+                w0[j] = w1[j] = make_uint4(0, 0, 0, 0);
+                if (g + j < l && h < H) {
+                    w0[j] = *reinterpret_cast<const uint4*>(src(h) + v0 * N);
+                    w1[j] = *reinterpret_cast<const uint4*>(src(h) + v1 * N);
+                }
+            }
+            if (!have_angles) {
+                // While they are on their way: each lane takes the sines and
+                // cosines of pairs 2 lane and 2 lane + 1, and every thread
+                // fetches those of its own pairs from their lanes (16 shuffles
+                // in place of 6 more evaluations).
+                have_angles = true;
+                float2 mine[2];
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    mine[e] = make_float2(0.f, 1.f);
+                    if (2 * lane + e < a.rot / 2) mine[e] = sin_cos(pos, a.turn[2 * lane + e]);
+                    mine[e].x *= a.amplitude;
+                    mine[e].y *= a.amplitude;
+                }
+#pragma unroll
+                for (int i = 0; i < N; i += 2) {
+                    const int pair = HALF ? c * N + i : (i < N / 2 ? v0 * (N / 2) + i : v1 * (N / 2) + i - N / 2);
+                    const int from = (pair >> 1) & 31;  // pair is even
+                    sn[i / 2] = f32x2(__shfl_sync(0xffffffffu, mine[0].x, from), __shfl_sync(0xffffffffu, mine[1].x, from));
+                    cs[i / 2] = f32x2(__shfl_sync(0xffffffffu, mine[0].y, from), __shfl_sync(0xffffffffu, mine[1].y, from));
+                }
+            }
+            float ss[BATCH];
+            if (a.q_weight || a.k_weight) {  // the shuffles of the batch overlap
+#pragma unroll
+                for (int j = 0; j < BATCH; ++j) {
+                    uint64_t x1[N / 2], x2[N / 2];
+                    P::unpack(w0[j], w1[j], x1, x2);
+                    uint64_t s1 = f32x2(0.f, 0.f), s2 = s1;
+#pragma unroll
+                    for (int i = 0; i < N / 2; ++i) {
+                        s1 = fma_f32x2(x1[i], x1[i], s1);
+                        s2 = fma_f32x2(x2[i], x2[i], s2);
+                    }
+                    const float2 s = f32x2_split(add_f32x2(s1, s2));
+                    ss[j] = s.x + s.y;
+                }
+#pragma unroll
+                for (int off = TPH / 2; off > 0; off >>= 1)
+#pragma unroll
+                    for (int j = 0; j < BATCH; ++j) ss[j] += __shfl_xor_sync(0xffffffffu, ss[j], off);
+            }
+#pragma unroll
+            for (int j = 0; j < BATCH; ++j) {
+                const int h = (g + j) * HPW + lane / TPH;
+                const int key = is_key(h);
+                const T* weight = static_cast<const T*>(key ? a.k_weight : a.q_weight);
+                uint64_t x1[N / 2], x2[N / 2];
+                P::unpack(w0[j], w1[j], x1, x2);
+                if (weight) {
+                    if (weight_kind != key) {
+                        q0 = *reinterpret_cast<const uint4*>(weight + v0 * N);
+                        q1 = *reinterpret_cast<const uint4*>(weight + v1 * N);
+                        weight_kind = key;
+                    }
+                    const float r = rsqrtf(ss[j] * (1.f / D) + a.eps);
+                    const uint64_t rr = f32x2(r, r);
+                    uint64_t y1[N / 2], y2[N / 2];
+                    P::unpack(q0, q1, y1, y2);
+#pragma unroll
+                    for (int i = 0; i < N / 2; ++i) {
+                        x1[i] = mul_f32x2(mul_f32x2(x1[i], rr), y1[i]);
+                        x2[i] = mul_f32x2(mul_f32x2(x2[i], rr), y2[i]);
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < N / 2; ++i) {
+                    if (HALF || i < N / 4 ? r0 : r1) {
+                        const uint64_t z1 = x1[i], z2 = x2[i];
+                        const float2 n2 = f32x2_split(z2);
+                        x1[i] = fma_f32x2(f32x2(-n2.x, -n2.y), sn[i], mul_f32x2(z1, cs[i]));
+                        x2[i] = fma_f32x2(z1, sn[i], mul_f32x2(z2, cs[i]));
+                    }
+                }
+                // A vector that is neither normalised nor rotated keeps its bits.
+                uint4 o0, o1;
+                P::pack(x1, x2, o0, o1);
+                if (weight || r0) w0[j] = o0;
+                if (weight || r1) w1[j] = o1;
+                if (g + j < l && h < H) {
+                    *reinterpret_cast<uint4*>(dst(h) + v0 * N) = w0[j];
+                    *reinterpret_cast<uint4*>(dst(h) + v1 * N) = w1[j];
+                }
             }
         }
-        return r;
     };
-    Group next = load(g0);
-    float2 sc[N];  // sin, cos: pair by pair
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-        const int pair = HALF ? c * N + i : (i < N / 2 ? v0 * (N / 2) + i : v1 * (N / 2) + i - N / 2);
-        const bool on = HALF ? r0 : (i < N / 2 ? r0 : r1);
-        sc[i] = make_float2(0.f, 1.f);
-        if (on) {
-            sc[i] = sin_cos(pos, a.turn[pair]);
-            sc[i].x *= a.amplitude;
-            sc[i].y *= a.amplitude;
+    {
+        const T* const src_q = static_cast<const T*>(a.q) + static_cast<int64_t>(t) * a.q_stride;
+        const T* const src_k = static_cast<const T*>(a.k) + static_cast<int64_t>(t) * a.k_stride;
+        T* const dst_q = static_cast<T*>(a.q_out) + static_cast<int64_t>(t) * a.qo_stride;
+        T* const dst_k = static_cast<T*>(APPEND ? a.kpool : a.k_out) + at;
+        if constexpr (WHOLE) {
+            // Whole groups of queries, then of keys: nothing to select per head.
+            const int nq = a.Hq / HPW;
+            turn([](int) { return 0; }, [&](int h) { return src_q + h * D; }, [&](int h) { return dst_q + h * D; },
+                 a.Hq, min(g0, nq), min(g1, nq));
+            turn([](int) { return 1; }, [&](int h) { return src_k + h * D; },
+                 [&](int h) { return dst_k + static_cast<int64_t>(h) * kv_step; }, a.Hk, max(g0 - nq, 0),
+                 min(g1, rotated) - nq);
+        } else {
+            turn([&](int h) { return h < a.Hq ? 0 : 1; },
+                 [&](int h) { return h < a.Hq ? src_q + h * D : src_k + (h - a.Hq) * D; },
+                 [&](int h) { return h < a.Hq ? dst_q + h * D : dst_k + static_cast<int64_t>(h - a.Hq) * kv_step; },
+                 a.Hq + a.Hk, g0, min(g1, rotated));
         }
     }
-    // The vectors of the next group are on their way while one is worked on.
-    for (int g = g0; g < g1; ++g) {
-        const Group now = next;
-        if (g + 1 < g1) next = load(g + 1);
-        const bool is_q = now.kind == 0, turn = now.kind <= 1;
-        const T* weight = static_cast<const T*>(is_q ? a.q_weight : now.kind == 1 ? a.k_weight : nullptr);
-        float x[2 * N];
-        Vec<T>::unpack(now.w0, x);
-        Vec<T>::unpack(now.w1, x + N);
-        const bool norm = weight != nullptr;
-        if (__any_sync(0xffffffffu, norm)) {
-            float ss = 0.f;
+    if constexpr (APPEND) {
+        // The values' groups: copied, vector by vector.
+        constexpr int VPH = D / N;  // vectors a head
+        const T* const src = static_cast<const T*>(a.v) + static_cast<int64_t>(t) * a.v_stride;
+        T* const dst = static_cast<T*>(a.vpool) + at;
+        const int end = min(g1 - rotated, (a.Hk + HPW - 1) / HPW) * HPW * VPH;
+        for (int i = max(g0 - rotated, 0) * HPW * VPH + lane; i < end; i += 32 * 4) {
+            uint4 w[4];
 #pragma unroll
-            for (int i = 0; i < 2 * N; ++i) ss = fmaf(x[i], x[i], ss);
+            for (int j = 0; j < 4; ++j)
+                if (i + 32 * j < min(end, a.Hk * VPH)) w[j] = *reinterpret_cast<const uint4*>(src + (i + 32 * j) * N);
 #pragma unroll
-            for (int off = TPH / 2; off > 0; off >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, off);
-            if (norm) {
-                const float r = rsqrtf(ss * (1.f / D) + a.eps);
-                float wt[2 * N];
-                Vec<T>::unpack(*reinterpret_cast<const uint4*>(weight + v0 * N), wt);
-                Vec<T>::unpack(*reinterpret_cast<const uint4*>(weight + v1 * N), wt + N);
-#pragma unroll
-                for (int i = 0; i < 2 * N; ++i) x[i] *= r * wt[i];
+            for (int j = 0; j < 4; ++j) {
+                const int h = (i + 32 * j) / VPH, e = (i + 32 * j) % VPH;
+                if (i + 32 * j < min(end, a.Hk * VPH))
+                    *reinterpret_cast<uint4*>(dst + static_cast<int64_t>(h) * kv_step + e * N) = w[j];
             }
-        }
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
-            const int e1 = HALF ? i : 2 * i, e2 = HALF ? i + N : 2 * i + 1;
-            const bool rot = turn && (HALF ? r0 : (i < N / 2 ? r0 : r1));
-            const float x1 = x[e1], x2 = x[e2];
-            if (rot) {
-                x[e1] = x1 * sc[i].y - x2 * sc[i].x;
-                x[e2] = x2 * sc[i].y + x1 * sc[i].x;
-            }
-        }
-        // A vector that is neither normalised nor rotated keeps its bits.
-        const uint4 w0 = norm || (turn && r0) ? Vec<T>::pack(x) : now.w0;
-        const uint4 w1 = norm || (turn && r1) ? Vec<T>::pack(x + N) : now.w1;
-        if (now.kind < 3) {
-            *reinterpret_cast<uint4*>(now.dst + v0 * N) = w0;
-            *reinterpret_cast<uint4*>(now.dst + v1 * N) = w1;
         }
     }
 }
 
 using RopeFn = void (*)(RopeArgs);
 
-template <bool APPEND>
+template <bool APPEND, int BATCH, int BLOCKS, bool WHOLE>
 RopeFn rope_select(int D, bool bf16, bool half) {
-    if (bf16) {
-        if (D == 128) return half ? rope_kernel<uint16_t, 128, true, APPEND> : rope_kernel<uint16_t, 128, false, APPEND>;
-        return half ? rope_kernel<uint16_t, 64, true, APPEND> : rope_kernel<uint16_t, 64, false, APPEND>;
-    }
-    if (D == 128) return half ? rope_kernel<float, 128, true, APPEND> : rope_kernel<float, 128, false, APPEND>;
-    return half ? rope_kernel<float, 64, true, APPEND> : rope_kernel<float, 64, false, APPEND>;
+    if (bf16 && D == 128)
+        return half ? rope_kernel<uint16_t, 128, true, APPEND, BATCH, BLOCKS, WHOLE>
+                    : rope_kernel<uint16_t, 128, false, APPEND, BATCH, BLOCKS, WHOLE>;
+    if (bf16)
+        return half ? rope_kernel<uint16_t, 64, true, APPEND, BATCH, BLOCKS, WHOLE>
+                    : rope_kernel<uint16_t, 64, false, APPEND, BATCH, BLOCKS, WHOLE>;
+    if (D == 128)
+        return half ? rope_kernel<float, 128, true, APPEND, BATCH, BLOCKS, WHOLE>
+                    : rope_kernel<float, 128, false, APPEND, BATCH, BLOCKS, WHOLE>;
+    return half ? rope_kernel<float, 64, true, APPEND, BATCH, BLOCKS, WHOLE>
+                : rope_kernel<float, 64, false, APPEND, BATCH, BLOCKS, WHOLE>;
 }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
@@ -280,16 +382,28 @@ pa_status rope_args(RopeArgs* a, const void* q, int64_t q_stride, const void* k,
     return PA_OK;
 }
 
-pa_status rope_launch(RopeArgs* a, RopeFn fn, int heads, int D, int elem, cudaStream_t stream) {
+template <bool APPEND>
+pa_status rope_launch(RopeArgs* a, int D, bool bf16, bool half, cudaStream_t stream) {
     if (a->T == 0) return PA_OK;
-    const int hpw = 32 / (D / (32 / elem));
-    const int groups = (heads + hpw - 1) / hpw;
+    const int hpw = 32 / (D / (32 / (bf16 ? 2 : 4)));
+    const int groups = (a->Hq + a->Hk + hpw - 1) / hpw + (APPEND ? (a->Hk + hpw - 1) / hpw : 0);
     // One warp a row, all its heads, once the rows alone fill the SMs; more
     // warps a row, each with fewer heads, before that.
-    const int64_t fill = 152LL * 32;
+    const int64_t fill = static_cast<int64_t>(kSms) * 16;
     a->wpt = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(groups, (fill + a->T - 1) / a->T)));
     a->gpw = (groups + a->wpt - 1) / a->wpt;
     a->wpt = (groups + a->gpw - 1) / a->gpw;
+    // Queries and keys in loops of their own where both fill whole groups and
+    // the queries alone a few of them (32768 rows of 32 + 8 + 8 heads with norms
+    // 135 against 146 us); one loop over both otherwise (32768 rows of 4 + 4
+    // heads 35 against 42 us), so that few heads still share a batch of loads.
+    // Loads in flight: four groups, or two beside the norm's and the pools'
+    // registers (16421 rows of 32 + 8 heads 51.9 us with four and 52.9 with
+    // two; the 32768 rows above 135.2 us with two and 136.6 with four).
+    const bool whole = a->Hq % hpw == 0 && a->Hk % hpw == 0 && a->Hq >= 4 * hpw;
+    const RopeFn fn = a->gpw == 1 ? rope_select<APPEND, 1, 1, false>(D, bf16, half)
+                      : whole     ? rope_select<APPEND, APPEND ? 2 : 4, 5, true>(D, bf16, half)
+                                  : rope_select<APPEND, 2, 5, false>(D, bf16, half);
     const int64_t blocks = (static_cast<int64_t>(a->T) * a->wpt + kRopeWarps - 1) / kRopeWarps;
     if (blocks > INT32_MAX) return PA_ERR_SHAPE;
     cudaLaunchConfig_t cfg = {};
@@ -382,9 +496,8 @@ pa_status pa_qk_rope(const void* q, int64_t q_stride, const void* k, int64_t k_s
     if (!pa::aligned16(k_out)) return PA_ERR_ALIGN;
     a.k_out = k_out;
     a.ko_stride = k_out_stride;
-    return pa::rope_launch(&a, pa::rope_select<false>(D, dtype == PA_BF16,
-                                                      !rope || rope->layout == PA_ROPE_HALF),
-                           Hq + Hk, D, elem, reinterpret_cast<cudaStream_t>(stream));
+    return pa::rope_launch<false>(&a, D, dtype == PA_BF16, !rope || rope->layout == PA_ROPE_HALF,
+                                  reinterpret_cast<cudaStream_t>(stream));
 }
 
 pa_status pa_qk_rope_append(const void* q, int64_t q_stride, const void* k, int64_t k_stride,
@@ -412,9 +525,8 @@ pa_status pa_qk_rope_append(const void* q, int64_t q_stride, const void* k, int6
     a.num_slots = static_cast<int64_t>(num_blocks) * block_size;
     a.err = device_error;
     if (num_rows > 0 && !a.err && pa::append_error_address(&a.err) != cudaSuccess) return PA_ERR_CUDA;
-    return pa::rope_launch(&a, pa::rope_select<true>(D, dtype == PA_BF16,
-                                                     !rope || rope->layout == PA_ROPE_HALF),
-                           Hq + 2 * Hkv, D, elem, reinterpret_cast<cudaStream_t>(stream));
+    return pa::rope_launch<true>(&a, D, dtype == PA_BF16, !rope || rope->layout == PA_ROPE_HALF,
+                                 reinterpret_cast<cudaStream_t>(stream));
 }
 
 }  // extern "C"

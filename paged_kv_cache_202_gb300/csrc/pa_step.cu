@@ -224,7 +224,7 @@ extern "C" pa_status pa_step_maps(const int32_t* cache_lens, const int32_t* new_
     a.T = num_rows;
     cudaLaunchConfig_t cfg = {};
     const int64_t want = (static_cast<int64_t>(num_rows) + pa::kStepThreads - 1) / pa::kStepThreads;
-    cfg.gridDim = dim3(static_cast<unsigned>(std::max<int64_t>(1, std::min<int64_t>(want, 152))));
+    cfg.gridDim = dim3(static_cast<unsigned>(std::max<int64_t>(1, std::min<int64_t>(want, pa::kSms))));
     cfg.blockDim = dim3(pa::kStepThreads);
     cfg.dynamicSmemBytes = (2 * static_cast<size_t>(B) + 1) * 4;
     cfg.stream = reinterpret_cast<cudaStream_t>(stream);
