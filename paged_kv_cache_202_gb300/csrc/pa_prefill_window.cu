@@ -458,7 +458,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             // The whole warp runs this loop and one thread issues: with the loop
             // in one thread every product took 87 cycles to issue, its operands
             // moved to uniform registers each time.
-            const uint32_t one = tc::elect_one();
+            const uint32_t one = elect_one();
             const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
             const uint32_t hi = static_cast<uint32_t>(tc::smem_desc(base, 16, 1024) >> 32);
             const uint32_t lo_q = tc::desc_lo(base + kOffQ, 16);

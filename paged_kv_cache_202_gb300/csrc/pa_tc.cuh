@@ -109,17 +109,6 @@ __device__ __forceinline__ void commit_if(uint32_t issue, uint32_t mbar) {
         : "memory");
 }
 
-// 1 in one thread of the (converged) warp, the same one every time.
-__device__ __forceinline__ uint32_t elect_one() {
-    uint32_t r;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "elect.sync _|p, 0xffffffff;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(r));
-    return r;
-}
-
 __device__ __forceinline__ uint32_t desc_lo(uint32_t addr, uint32_t lbo) {
     return ((addr >> 4) & 0x3FFFu) | (((lbo >> 4) & 0x3FFFu) << 16);
 }

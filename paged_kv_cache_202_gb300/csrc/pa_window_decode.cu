@@ -121,7 +121,8 @@ __global__ void __launch_bounds__(32 * kWarpsPerSm, 1)
     constexpr int CP = CT / BS;                       // pages per chunk
     constexpr uint32_t kStage = 2u * CT * D * 2u;     // K and V of a chunk
     extern __shared__ uint8_t smem_raw[];
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, W = blockDim.x >> 5;
+    const int tid = threadIdx.x, lane = tid & 31, W = blockDim.x >> 5;
+    const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
     const uint32_t raw = smem_addr(smem_raw);
     const uint32_t base = (raw + 1023u) & ~1023u;
     uint8_t* const gbase = smem_raw + (base - raw);
@@ -177,6 +178,7 @@ __global__ void __launch_bounds__(32 * kWarpsPerSm, 1)
     __syncthreads();
 
     bool poison = false;
+    const uint32_t one = elect_one();
     // Copies the chunk's pages into the warp's stage; false if one is outside the pool.
     auto issue = [&](int chunk, int page) {
         const int n = min(CP, nb - chunk * CP);
@@ -185,17 +187,17 @@ __global__ void __launch_bounds__(32 * kWarpsPerSm, 1)
             if (lane == 0) atomicOr(a.err, kErrTable);
             return false;
         }
-        if (lane == 0) mbar_arrive_expect_tx(bar, n * (2u * BS * D * 2u));
+        if (one) mbar_arrive_expect_tx(bar, n * (2u * BS * D * 2u));
+        __syncwarp();
 #pragma unroll
         for (int j = 0; j < CP; ++j) {
             const int r = __shfl_sync(0xffffffffu, page, j) * a.Hkv + kvh;
-            if (j < n && lane == 0) {
+            const uint32_t on = j < n ? one : 0u;
 #pragma unroll
-                for (int h = 0; h < D / 64; ++h) {
-                    const uint32_t off = h * (CT * 128) + j * (BS * 128);
-                    tma_load_3d_plain(stg + off, &kmap, h * 64, 0, r, bar);
-                    tma_load_3d_plain(stg + CT * D * 2 + off, &vmap, h * 64, 0, r, bar);
-                }
+            for (int h = 0; h < D / 64; ++h) {
+                const uint32_t off = h * (CT * 128) + j * (BS * 128);
+                tma_load_3d_if(on, stg + off, &kmap, h * 64, 0, r, bar);
+                tma_load_3d_if(on, stg + CT * D * 2 + off, &vmap, h * 64, 0, r, bar);
             }
         }
         return true;
