@@ -377,8 +377,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     if (warp >= kWarpLoad) {
 
-        if ((warp == kWarpLoad || warp == kWarpLoadV) && lane == 0) {
+        if (warp == kWarpLoad || warp == kWarpLoadV) {
             // ------------------------------------------------------------ copies (Q and K, V)
+            // The whole warp runs this loop and one thread issues, as below: from
+            // one thread the 16 boxes of a chunk took 1,900 cycles.
+            const uint32_t one = elect_one();
             const bool is_k = warp == kWarpLoad;
             const int nst = is_k ? kStagesK : kStagesV;
             const uint32_t full = bars + (is_k ? kBarKFull : kBarVFull);
@@ -387,58 +390,67 @@ __global__ void __launch_bounds__(kThreads, 1)
             const CUtensorMap* map = is_k ? &kmap : &vmap;
             const int sink_pages = (a.sinks + BS - 1) / BS;
             constexpr int kPages = kChunk / BS;
+            auto wait = [&](uint32_t bar, uint32_t parity) {
+                return __all_sync(0xffffffffu, wait_role(bar, parity, abort_flag, a.err)) != 0;
+            };
             // K/V pages of an item are read again for the item's neighbours:
             // no eviction hint, unlike the kernels that read a page once.
             Walk w(a);
-            int issued = 0;          // chunks, over all items: the ring's count
-            int nq_loads[2] = {0, 0};  // query tiles copied
+            int s = 0;                 // ring stage
+            uint32_t parity = 1;       // of its last release: a fresh stage counts as released
+            int issued = 0;            // chunks in the ring, at most nst
+            uint32_t qp[2] = {1, 1};   // the query buffers, likewise
+            int q_used = 0;            // bit u: buffer u holds or awaits a tile
             bool ok = true;
             while (ok && w.next()) {
                 const int32_t* table = a.tables + static_cast<size_t>(w.it.b) * a.max_blocks;
-                const int nb = (w.it.len + BS - 1) / BS;
-                for (int c = 0; c < w.nc; ++c) {
-                    int pg[kPages];
-#pragma unroll
-                    for (int j = 0; j < kPages; ++j) {
-                        const int p = c * kPages + j;
-                        pg[j] = p < nb ? table[p < sink_pages ? p : p + w.it.skip] : 0;
-                    }
-                    const int s = issued % nst;
-                    if (issued >= nst && !wait_role(empty + 8 * s, ((issued / nst) - 1) & 1, abort_flag, a.err)) {
-                        ok = false;
-                        break;
-                    }
+                const int nb = __shfl_sync(0xffffffffu, (w.it.len + BS - 1) / BS, 0);
+                const int nc = __shfl_sync(0xffffffffu, w.nc, 0), h = __shfl_sync(0xffffffffu, w.h, 0);
+                // Lane j: the block of page j of chunk c, one chunk ahead.
+                auto entries = [&](int c) {
+                    const int p = c * kPages + lane;
+                    return lane < kPages && p < nb ? table[p < sink_pages ? p : p + w.it.skip] : 0;
+                };
+                int pg = entries(0);
+                for (int c = 0; c < nc; ++c) {
+                    const int pg_next = c + 1 < nc ? entries(c + 1) : 0;
+                    ok = wait(empty + 8 * s, parity);
+                    if (!ok) break;
                     const int np = min(kPages, nb - c * kPages);
                     const uint32_t bar = full + 8 * s, stage = ring + s * kStageKV;
-                    mbar_arrive_expect_tx(bar, static_cast<uint32_t>(np) * BS * kD * 2);
+                    if (one) mbar_arrive_expect_tx(bar, static_cast<uint32_t>(np) * BS * kD * 2);
+                    __syncwarp();
 #pragma unroll
                     for (int j = 0; j < kPages; ++j) {
-                        if (j < np) {
-                            const int r = pg[j] * a.Hkv + w.h;
+                        const int r = __shfl_sync(0xffffffffu, pg, j) * a.Hkv + h;
+                        const uint32_t on = j < np ? one : 0u;
 #pragma unroll
-                            for (int hf = 0; hf < 2; ++hf)
-                                tma_load_3d_plain(stage + hf * kHalfKV + j * BS * 128, map, hf * 64, 0, r, bar);
-                        }
+                        for (int hf = 0; hf < 2; ++hf)
+                            tma_load_3d_if(on, stage + hf * kHalfKV + j * BS * 128, map, hf * 64, 0, r, bar);
                     }
-                    ++issued;
+                    pg = pg_next;
+                    issued = min(issued + 1, nst);
+                    if (++s == nst) s = 0, parity ^= 1u;
                     if (is_k && c == 0) {
                         // The item's queries behind its first keys (whose stage
                         // is free before the queries' buffer is): one box per
                         // 64-column half, rows in (query, head) order. Rows past
                         // the item's queries hold other rows of q or zeros; they
                         // are never stored.
-                        for (int u = 0; u < (w.it.nq > a.Qb ? 2 : 1) && ok; ++u) {
-                            const int n = nq_loads[u]++;
-                            if (n > 0 && !wait_role(bars + kBarQEmpty + 8 * u, (n - 1) & 1, abort_flag, a.err)) {
-                                --nq_loads[u];
-                                ok = false;
-                                break;
-                            }
-                            mbar_arrive_expect_tx(bars + kBarQFull + 8 * u, kTileQ);
+                        const int row = __shfl_sync(0xffffffffu, w.it.row, 0);
+                        const int tiles = __shfl_sync(0xffffffffu, w.it.nq > a.Qb ? 2 : 1, 0);
+                        for (int u = 0; u < tiles && ok; ++u) {
+                            ok = wait(bars + kBarQEmpty + 8 * u, qp[u]);
+                            if (!ok) break;
+                            qp[u] ^= 1u;
+                            q_used |= 1 << u;
+                            const uint32_t qbar = bars + kBarQFull + 8 * u;
+                            if (one) mbar_arrive_expect_tx(qbar, kTileQ);
+                            __syncwarp();
 #pragma unroll
                             for (int hf = 0; hf < 2; ++hf)
-                                tma_load_3d_plain(base + kOffQ + u * kTileQ + hf * 16384, &qmap, hf * 64,
-                                                  w.h * a.g, w.it.row + u * a.Qb, bars + kBarQFull + 8 * u);
+                                tma_load_3d_if(one, base + kOffQ + u * kTileQ + hf * 16384, &qmap, hf * 64, h * a.g,
+                                               row + u * a.Qb, qbar);
                         }
                         if (!ok) break;
                     }
@@ -447,12 +459,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             // Copies still in flight land before the block leaves: the last
             // chunk issued on each stage and the last tile of each query
             // buffer. Without an abort their consumers have waited for them.
-            for (int k = max(0, issued - nst); k < issued; ++k)
-                mbar_wait_bounded(full + 8 * (k % nst), (k / nst) & 1, kWaitLimitNs);
+            for (int i = 0; i < issued; ++i) {
+                if (--s < 0) s = nst - 1, parity ^= 1u;
+                mbar_wait_bounded(full + 8 * s, parity ^ 1u, kWaitLimitNs);
+            }
             if (is_k)
                 for (int u = 0; u < 2; ++u)
-                    if (nq_loads[u] > 0)
-                        mbar_wait_bounded(bars + kBarQFull + 8 * u, (nq_loads[u] - 1) & 1, kWaitLimitNs);
+                    if (q_used >> u & 1) mbar_wait_bounded(bars + kBarQFull + 8 * u, qp[u], kWaitLimitNs);
         } else if (warp == kWarpMma) {
             // ------------------------------------------------------------ products
             // The whole warp runs this loop and one thread issues: with the loop
