@@ -545,8 +545,9 @@ pa_status pa_decode_noalloc(const void* q, const void* k_pool, const void* v_poo
  * (taken as 0), raises PA_DEVERR_TABLE; the slots it concerns are -1, the
  * table entry is written as it is and later calls refuse it. seq_lens and
  * q_start must not overlap cache_lens or new_lens, nor free_left free_count
- * (PA_ERR_SHAPE): chained steps alternate between two buffers. B = 0 is a
- * no-op. One launch; results do not depend on timing.
+ * (PA_ERR_SHAPE): chained steps alternate between two buffers. Pointers not
+ * aligned to their elements return PA_ERR_ALIGN. B = 0 is a no-op. One launch;
+ * results do not depend on timing.
  */
 pa_status pa_step_maps(const int32_t* cache_lens, const int32_t* new_lens, int B,
                        const int32_t* free_blocks, int num_free, const int32_t* free_count,
@@ -669,9 +670,9 @@ pa_status pa_qk_rope_append(const void* q, int64_t q_stride, const void* k, int6
  * pa_decode's split kernels and the plan's workspace. Calls on one plan must be
  * ordered on the device (one stream, or events). A call that has to create the
  * plan or needs a larger workspace during a stream capture returns
- * PA_ERR_WORKSPACE: make the call once before capturing it. Memory that this
- * call and pa_prefill_window outgrow is kept until pa_free, so graphs captured
- * with the plan stay valid.
+ * PA_ERR_WORKSPACE: make the call once before capturing it. Once a windowed
+ * call has used the plan's workspace, memory that a later call outgrows is kept
+ * until pa_free, so graphs captured with the plan stay valid.
  */
 pa_status pa_decode_window(const void* q, const void* k_pool, const void* v_pool,
                            const int32_t* block_tables, int max_blocks, const int32_t* seq_lens,

@@ -457,23 +457,32 @@ class Rope:
         self.address = ctypes.addressof(self.struct)   # what the calls pass; the struct stays with self
 
 
-# A decode step makes these calls once a layer, on a few rows: the checks are
-# what the call costs. Each argument is checked in one expression of attribute
-# reads that is true for what the call takes; _refuse then finds out what is
-# wrong with one that is not. (One call of pa_step_maps: 17 us with a helper
-# per property and torch.cuda.current_stream, of which the library's call is
-# 3.5 us; 9 us this way.)
+# A decode step makes these calls once a layer, on a few rows, and the checks are
+# most of what a call costs the host. So each function checks all its arguments
+# in one expression of attribute reads that holds for what it takes, and looks
+# for the argument that is wrong, to name it, only when it does not. (One call of
+# pa_step_maps: 17 us with a helper per property and torch.cuda.current_stream,
+# 8 us this way, of which the library's call is 3.6 us.)
 
-def _refuse(what: str, name: str, t: torch.Tensor, dev: int, shape: tuple, dtype: torch.dtype):
-    if not t.is_cuda:
-        raise ValueError(f"{what}: {name}: tensors must be on a CUDA device")
-    if t.get_device() != dev:
-        raise ValueError(f"{what}: {name} is on {t.device}, not on device {dev}: all must be on one device")
-    if t.dtype != dtype:
-        raise TypeError(f"{what}: {name} is {t.dtype}, expected {dtype}")
-    if tuple(t.shape) != shape:
-        raise ValueError(f"{what}: {name} has shape {tuple(t.shape)}, expected {shape}")
-    raise ValueError(f"{what}: {name} must be contiguous")
+def _refuse(what: str, dev: int, args) -> None:
+    """Raise for the first of (name, tensor, shape, dtype) that is not on device
+    ``dev``, of that type and shape, and contiguous (None: rows may be strided)."""
+    if dev < 0:
+        raise ValueError(f"{what}: tensors must be on a CUDA device")
+    for name, t, shape, dtype, *rows in args:
+        if t is None:
+            continue
+        if not t.is_cuda:
+            raise ValueError(f"{what}: {name}: tensors must be on a CUDA device")
+        if t.get_device() != dev:
+            raise ValueError(f"{what}: {name} is on {t.device}, not on device {dev}: all must be on one device")
+        if t.dtype != dtype:
+            raise TypeError(f"{what}: {name} is {t.dtype}, expected {dtype}")
+        if tuple(t.shape) != tuple(shape):
+            raise ValueError(f"{what}: {name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+        if not rows and not t.is_contiguous():
+            raise ValueError(f"{what}: {name} must be contiguous")
+    raise ValueError(f"{what}: unsupported tensors")
 
 
 def _call(what: str, fn, dev: int, stream, *args) -> None:
@@ -482,7 +491,7 @@ def _call(what: str, fn, dev: int, stream, *args) -> None:
         stream = torch._C._cuda_getCurrentRawStream(dev)
     elif hasattr(stream, "cuda_stream"):
         stream = stream.cuda_stream
-    if dev == torch.cuda.current_device():
+    if dev == torch._C._cuda_getDevice():
         st = fn(*args, stream)
     else:
         with torch.cuda.device(dev):
@@ -491,27 +500,22 @@ def _call(what: str, fn, dev: int, stream, *args) -> None:
         raise PagedAttentionError(st, what)
 
 
-def _rows(what: str, name: str, t: torch.Tensor, dev: int, shape: tuple, dtype: torch.dtype) -> int:
-    """The row stride of [rows, H, D] rows whose heads are contiguous."""
-    if t.dtype is not dtype or t.get_device() != dev or t.shape != shape:
-        _refuse(what, name, t, dev, shape, dtype)
-    T, H, D = shape
+def _rows(what: str, name: str, t: torch.Tensor, T: int, H: int, D: int) -> int:
+    """The row stride of [T, H, D] rows whose heads are contiguous."""
     s0, s1, s2 = t.stride()
     if s2 != 1 or (s1 != D and H > 1):
         raise ValueError(f"{what}: {name}: the heads of a row must be contiguous")
     return s0 if T > 1 else H * D
 
 
+def _error(what: str, t: torch.Tensor | None, dev: int) -> int | None:
+    if t is not None and t.get_device() != dev:
+        raise ValueError(f"{what}: device_error is on {t.device}, not on device {dev}: all must be on one device")
+    return _error_word(t)
+
+
 _I32, _I64 = torch.int32, torch.int64
 _INT_MAX = 2 ** 31 - 1   # a C int would drop the upper bits of more; bounds and windows saturate
-
-
-def _weight(what: str, name: str, t: torch.Tensor | None, dev: int, D: int, dtype: torch.dtype) -> int | None:
-    if t is None:
-        return None
-    if t.dtype is not dtype or t.get_device() != dev or t.shape != (D,) or not t.is_contiguous():
-        _refuse(what, name, t, dev, (D,), dtype)
-    return t.data_ptr()
 
 
 def pa_step_maps(cache_lens: torch.Tensor, new_lens: torch.Tensor, free_blocks: torch.Tensor,
@@ -526,33 +530,36 @@ def pa_step_maps(cache_lens: torch.Tensor, new_lens: torch.Tensor, free_blocks: 
     ``free_blocks`` is a stack of free block ids of which ``free_count`` [1]
     are valid; ``slots`` may have more rows than the step (padding: slot -1).
     """
-    what = "pa_step_maps"
     B, T, F = cache_lens.shape[0], slots.shape[0], free_blocks.shape[0]
     MB = block_tables.shape[-1]
     dev = cache_lens.get_device()
-    for name, t, shape in (("cache_lens", cache_lens, (B,)), ("new_lens", new_lens, (B,)),
-                           ("free_blocks", free_blocks, (F,)), ("free_count", free_count, (1,)),
-                           ("block_tables", block_tables, (B, MB)), ("seq_lens", seq_lens, (B,)),
-                           ("q_start", q_start, (B + 1,)), ("positions", positions, (T,)),
-                           ("free_left", free_left, (1,))):
-        if t.dtype is not _I32 or t.get_device() != dev or t.shape != shape or not t.is_contiguous():
-            _refuse(what, name, t, dev, shape, _I32)
-    if slots.dtype is not _I64 or slots.get_device() != dev or not slots.is_contiguous() or slots.dim() != 1:
-        _refuse(what, "slots", slots, dev, (T,), _I64)
-    if dev < 0:
-        _refuse(what, "cache_lens", cache_lens, dev, (B,), _I32)
-    if T > _INT_MAX or F > _INT_MAX or B > _INT_MAX:
-        raise ValueError(f"{what}: more than 2^31 - 1 rows, free blocks or requests")
-    err = None
-    if device_error is not None:
-        err = _error_word(device_error)
-        if device_error.get_device() != dev:
-            _refuse(what, "device_error", device_error, dev, (1,), _I32)
-    _call(what, lib().pa_step_maps, dev, stream, cache_lens.data_ptr(), new_lens.data_ptr(), B,
-          free_blocks.data_ptr() or free_count.data_ptr(), F, free_count.data_ptr(),
-          block_tables.data_ptr(), MB, int(block_size), int(num_blocks), min(int(max_seq_len), _INT_MAX),
-          seq_lens.data_ptr(),
-          q_start.data_ptr(), positions.data_ptr(), slots.data_ptr(), T, free_left.data_ptr(), err)
+    if not (cache_lens.dtype is new_lens.dtype is free_blocks.dtype is free_count.dtype
+            is block_tables.dtype is seq_lens.dtype is q_start.dtype is positions.dtype
+            is free_left.dtype is _I32 and slots.dtype is _I64
+            and dev == new_lens.get_device() == free_blocks.get_device() == free_count.get_device()
+            == block_tables.get_device() == seq_lens.get_device() == q_start.get_device()
+            == positions.get_device() == slots.get_device() == free_left.get_device() and dev >= 0
+            and cache_lens.shape == new_lens.shape == seq_lens.shape == (B,)
+            and positions.shape == slots.shape == (T,) and free_count.shape == free_left.shape == (1,)
+            and block_tables.shape == (B, MB) and q_start.shape == (B + 1,) and free_blocks.dim() == 1
+            and cache_lens.is_contiguous() and new_lens.is_contiguous() and free_blocks.is_contiguous()
+            and block_tables.is_contiguous() and seq_lens.is_contiguous() and q_start.is_contiguous()
+            and positions.is_contiguous() and slots.is_contiguous()
+            and T <= _INT_MAX and F <= _INT_MAX and B <= _INT_MAX):
+        _refuse("pa_step_maps", dev, (
+            ("cache_lens", cache_lens, (B,), _I32), ("new_lens", new_lens, (B,), _I32),
+            ("free_blocks", free_blocks, (F,), _I32), ("free_count", free_count, (1,), _I32),
+            ("block_tables", block_tables, (B, MB), _I32), ("seq_lens", seq_lens, (B,), _I32),
+            ("q_start", q_start, (B + 1,), _I32), ("positions", positions, (T,), _I32),
+            ("slots", slots, (T,), _I64), ("free_left", free_left, (1,), _I32)))
+    if B == 0:
+        return
+    err = None if device_error is None else _error("pa_step_maps", device_error, dev)
+    count = free_count.data_ptr()
+    _call("pa_step_maps", lib().pa_step_maps, dev, stream, cache_lens.data_ptr(), new_lens.data_ptr(), B,
+          free_blocks.data_ptr() or count, F, count, block_tables.data_ptr(), MB, int(block_size),
+          int(num_blocks), min(int(max_seq_len), _INT_MAX), seq_lens.data_ptr(), q_start.data_ptr(),
+          positions.data_ptr(), slots.data_ptr(), T, free_left.data_ptr(), err)
 
 
 def pa_qk_rope(q: torch.Tensor, k: torch.Tensor, positions: torch.Tensor, rope: Rope | None,
@@ -562,22 +569,29 @@ def pa_qk_rope(q: torch.Tensor, k: torch.Tensor, positions: torch.Tensor, rope: 
     into ``q_out`` and ``k_out``, which may be the inputs themselves. Rows may
     be strided (views of a fused projection); the heads of a row are contiguous."""
     what = "pa_qk_rope"
-    T, Hq, D = shape = q.shape
+    T, Hq, D = q.shape
     Hk = k.shape[1]
-    dt = q.dtype
-    dev = q.get_device()
-    qs, qos = _rows(what, "q", q, dev, shape, dt), _rows(what, "q_out", q_out, dev, shape, dt)
-    shape = (T, Hk, D)
-    ks, kos = _rows(what, "k", k, dev, shape, dt), _rows(what, "k_out", k_out, dev, shape, dt)
-    if (positions.dtype is not _I32 or positions.get_device() != dev or positions.shape != (T,)
-            or not positions.is_contiguous() or dev < 0):
-        _refuse(what, "positions", positions, dev, (T,), _I32)
+    dt, dev = q.dtype, q.get_device()
+    if not (dt is k.dtype is q_out.dtype is k_out.dtype and positions.dtype is _I32
+            and dev == k.get_device() == q_out.get_device() == k_out.get_device()
+            == positions.get_device() and dev >= 0 and q_out.shape == (T, Hq, D)
+            and k.shape == k_out.shape == (T, Hk, D) and positions.shape == (T,)
+            and positions.is_contiguous()
+            and (q_weight is None or (q_weight.dtype is dt and q_weight.get_device() == dev
+                                      and q_weight.shape == (D,) and q_weight.is_contiguous()))
+            and (k_weight is None or (k_weight.dtype is dt and k_weight.get_device() == dev
+                                      and k_weight.shape == (D,) and k_weight.is_contiguous()))):
+        _refuse(what, dev, (("k", k, (T, Hk, D), dt, 0), ("q_out", q_out, (T, Hq, D), dt, 0),
+                            ("k_out", k_out, (T, Hk, D), dt, 0), ("positions", positions, (T,), _I32),
+                            ("q_weight", q_weight, (D,), dt), ("k_weight", k_weight, (D,), dt)))
     if T == 0:
         return
-    _call(what, lib().pa_qk_rope, dev, stream, q.data_ptr(), qs, k.data_ptr(), ks,
-          positions.data_ptr(), T, Hq, Hk, D, _dtype(q), _weight(what, "q_weight", q_weight, dev, D, dt),
-          _weight(what, "k_weight", k_weight, dev, D, dt), float(eps),
-          None if rope is None else rope.address, q_out.data_ptr(), qos, k_out.data_ptr(), kos)
+    _call(what, lib().pa_qk_rope, dev, stream, q.data_ptr(), _rows(what, "q", q, T, Hq, D), k.data_ptr(),
+          _rows(what, "k", k, T, Hk, D), positions.data_ptr(), T, Hq, Hk, D, _dtype(q),
+          None if q_weight is None else q_weight.data_ptr(),
+          None if k_weight is None else k_weight.data_ptr(), float(eps),
+          None if rope is None else rope.address, q_out.data_ptr(), _rows(what, "q_out", q_out, T, Hq, D),
+          k_out.data_ptr(), _rows(what, "k_out", k_out, T, Hk, D))
 
 
 def pa_qk_rope_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, positions: torch.Tensor,
@@ -589,53 +603,53 @@ def pa_qk_rope_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, positio
     """``pa_qk_rope`` with the keys and values written to the paged pools at
     ``slots`` (int64 [T]; -1 marks a padding row, which is left alone)."""
     what = "pa_qk_rope_append"
-    T, Hq, D = shape = q.shape
-    NB, Hkv, bs, _ = pool = k_pool.shape
-    dt = q.dtype
-    dev = q.get_device()
-    qs, qos = _rows(what, "q", q, dev, shape, dt), _rows(what, "q_out", q_out, dev, shape, dt)
-    shape = (T, Hkv, D)
-    ks, vs = _rows(what, "k", k, dev, shape, dt), _rows(what, "v", v, dev, shape, dt)
-    pool = (NB, Hkv, bs, D)
-    for name, t in (("k_pool", k_pool), ("v_pool", v_pool)):
-        if t.dtype is not dt or t.get_device() != dev or t.shape != pool or not t.is_contiguous():
-            _refuse(what, name, t, dev, pool, dt)
-    if (positions.dtype is not _I32 or positions.get_device() != dev or positions.shape != (T,)
-            or not positions.is_contiguous() or dev < 0):
-        _refuse(what, "positions", positions, dev, (T,), _I32)
-    if (slots.dtype is not _I64 or slots.get_device() != dev or slots.shape != (T,)
-            or not slots.is_contiguous()):
-        _refuse(what, "slots", slots, dev, (T,), _I64)
-    err = None
-    if device_error is not None:
-        err = _error_word(device_error)
-        if device_error.get_device() != dev:
-            _refuse(what, "device_error", device_error, dev, (1,), _I32)
+    T, Hq, D = q.shape
+    NB, Hkv, bs, _ = k_pool.shape
+    dt, dev = q.dtype, q.get_device()
+    if not (dt is k.dtype is v.dtype is q_out.dtype is k_pool.dtype is v_pool.dtype
+            and positions.dtype is _I32 and slots.dtype is _I64
+            and dev == k.get_device() == v.get_device() == q_out.get_device() == k_pool.get_device()
+            == v_pool.get_device() == positions.get_device() == slots.get_device() and dev >= 0
+            and q_out.shape == (T, Hq, D) and k.shape == v.shape == (T, Hkv, D)
+            and k_pool.shape == v_pool.shape == (NB, Hkv, bs, D) and positions.shape == slots.shape == (T,)
+            and positions.is_contiguous() and slots.is_contiguous() and k_pool.is_contiguous()
+            and v_pool.is_contiguous()
+            and (q_weight is None or (q_weight.dtype is dt and q_weight.get_device() == dev
+                                      and q_weight.shape == (D,) and q_weight.is_contiguous()))
+            and (k_weight is None or (k_weight.dtype is dt and k_weight.get_device() == dev
+                                      and k_weight.shape == (D,) and k_weight.is_contiguous()))):
+        _refuse(what, dev, (("k", k, (T, Hkv, D), dt, 0), ("v", v, (T, Hkv, D), dt, 0),
+                            ("q_out", q_out, (T, Hq, D), dt, 0), ("k_pool", k_pool, (NB, Hkv, bs, D), dt),
+                            ("v_pool", v_pool, (NB, Hkv, bs, D), dt), ("positions", positions, (T,), _I32),
+                            ("slots", slots, (T,), _I64), ("q_weight", q_weight, (D,), dt),
+                            ("k_weight", k_weight, (D,), dt)))
+    err = None if device_error is None else _error(what, device_error, dev)
     if T == 0:
         return
-    _call(what, lib().pa_qk_rope_append, dev, stream, q.data_ptr(), qs, k.data_ptr(), ks,
-          v.data_ptr(), vs, positions.data_ptr(), slots.data_ptr(), T, Hq, Hkv, D, _dtype(q),
-          _weight(what, "q_weight", q_weight, dev, D, dt),
-          _weight(what, "k_weight", k_weight, dev, D, dt), float(eps),
-          None if rope is None else rope.address, q_out.data_ptr(), qos, k_pool.data_ptr(),
-          v_pool.data_ptr(), bs, NB, err)
+    _call(what, lib().pa_qk_rope_append, dev, stream, q.data_ptr(), _rows(what, "q", q, T, Hq, D),
+          k.data_ptr(), _rows(what, "k", k, T, Hkv, D), v.data_ptr(), _rows(what, "v", v, T, Hkv, D),
+          positions.data_ptr(), slots.data_ptr(), T, Hq, Hkv, D, _dtype(q),
+          None if q_weight is None else q_weight.data_ptr(),
+          None if k_weight is None else k_weight.data_ptr(), float(eps),
+          None if rope is None else rope.address, q_out.data_ptr(), _rows(what, "q_out", q_out, T, Hq, D),
+          k_pool.data_ptr(), v_pool.data_ptr(), bs, NB, err)
 
 
 def _check_window(what: str, q, k_pool, v_pool, block_tables, seq_lens, out, B: int) -> tuple:
-    """Devices, types and shapes of a windowed call: (device, Hkv, block size, blocks)."""
-    T, Hq, D = shape = q.shape
+    """Devices, types and shapes of a windowed call: (device, table width, blocks, Hkv, block size)."""
+    T, Hq, D = q.shape
     NB, Hkv, bs, _ = k_pool.shape
-    pool, MB, dt, dev = (NB, Hkv, bs, D), block_tables.shape[-1], q.dtype, q.get_device()
-    for name, t in (("k_pool", k_pool), ("v_pool", v_pool)):
-        if t.dtype is not dt or t.get_device() != dev or t.shape != pool or not t.is_contiguous():
-            _refuse(what, name, t, dev, pool, dt)
-    if out.get_device() != dev or out.shape != shape or not out.is_contiguous():
-        _refuse(what, "out", out, dev, tuple(shape), out.dtype)
-    if not q.is_contiguous() or dev < 0:
-        _refuse(what, "q", q, dev, tuple(shape), dt)
-    for name, t, shape in (("block_tables", block_tables, (B, MB)), ("seq_lens", seq_lens, (B,))):
-        if t.dtype is not _I32 or t.get_device() != dev or t.shape != shape or not t.is_contiguous():
-            _refuse(what, name, t, dev, shape, _I32)
+    MB, dt, dev = block_tables.shape[-1], q.dtype, q.get_device()
+    if not (dt is k_pool.dtype is v_pool.dtype and block_tables.dtype is seq_lens.dtype is _I32
+            and dev == k_pool.get_device() == v_pool.get_device() == block_tables.get_device()
+            == seq_lens.get_device() == out.get_device() and dev >= 0
+            and k_pool.shape == v_pool.shape == (NB, Hkv, bs, D) and out.shape == (T, Hq, D)
+            and block_tables.shape == (B, MB) and seq_lens.shape == (B,)
+            and q.is_contiguous() and k_pool.is_contiguous() and v_pool.is_contiguous()
+            and block_tables.is_contiguous() and seq_lens.is_contiguous() and out.is_contiguous()):
+        _refuse(what, dev, (("q", q, (T, Hq, D), dt), ("k_pool", k_pool, (NB, Hkv, bs, D), dt),
+                            ("v_pool", v_pool, (NB, Hkv, bs, D), dt), ("out", out, (T, Hq, D), out.dtype),
+                            ("block_tables", block_tables, (B, MB), _I32), ("seq_lens", seq_lens, (B,), _I32)))
     return dev, MB, NB, Hkv, bs
 
 
@@ -649,6 +663,8 @@ def pa_decode_window(q: torch.Tensor, k_pool: torch.Tensor, v_pool: torch.Tensor
     B, Hq, D = q.shape
     dev, MB, NB, Hkv, bs = _check_window("pa_decode_window", q, k_pool, v_pool, block_tables,
                                          seq_lens, out, B)
+    if B == 0:
+        return out
     _call("pa_decode_window", lib().pa_decode_window, dev, stream, q.data_ptr(),
           k_pool.data_ptr(), v_pool.data_ptr(), block_tables.data_ptr(), MB, seq_lens.data_ptr(), B,
           Hq, Hkv, D, bs, NB, min(int(max_seq_len), _INT_MAX), float(scale), min(int(window), _INT_MAX),
@@ -667,12 +683,13 @@ def pa_prefill_window(q: torch.Tensor, q_start: torch.Tensor, k_pool: torch.Tens
     T, Hq, D = q.shape
     B = seq_lens.shape[0]
     dev, MB, NB, Hkv, bs = _check_window(what, q, k_pool, v_pool, block_tables, seq_lens, out, B)
-    if (q_start.dtype is not _I32 or q_start.get_device() != dev or q_start.shape != (B + 1,)
-            or not q_start.is_contiguous()):
-        _refuse(what, "q_start", q_start, dev, (B + 1,), _I32)
+    if not (q_start.dtype is _I32 and q_start.get_device() == dev and q_start.shape == (B + 1,)
+            and q_start.is_contiguous()):
+        _refuse(what, dev, (("q_start", q_start, (B + 1,), _I32),))
     if T == 0 or B == 0:
         return out
-    _call(what, lib().pa_prefill_window, dev, stream, q.data_ptr(), q_start.data_ptr(), T, max_q,
+    _call(what, lib().pa_prefill_window, dev, stream, q.data_ptr(), q_start.data_ptr(), T,
+          min(int(max_q), _INT_MAX),
           k_pool.data_ptr(), v_pool.data_ptr(), block_tables.data_ptr(), MB, seq_lens.data_ptr(), B,
           Hq, Hkv, D, bs, NB, min(int(max_seq_len), _INT_MAX), float(scale), min(int(window), _INT_MAX),
           min(int(sinks), _INT_MAX), _dtype(q), out.data_ptr(),

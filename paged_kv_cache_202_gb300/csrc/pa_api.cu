@@ -306,7 +306,10 @@ struct pa_plan {
     int last_fused = 0;
     size_t cnt_clean = 0;  // bytes at the end of the workspace known to be zero
     int last_path = 0, last_blocks = 0, last_warps = 0;
-    std::vector<void*> retired;  // workspaces that a windowed call outgrew, kept for captured graphs
+    // After a windowed call, workspaces that a call outgrows are kept until
+    // pa_free: a captured graph may still use them.
+    bool keep = false;
+    std::vector<void*> retired;
     cudaEvent_t ev_start = nullptr, ev_stop = nullptr;
     MapKey kkey, vkey;
     CUtensorMap kmap, vmap;
@@ -355,10 +358,26 @@ pa_status pa_append_kv(const void* k_new, const void* v_new, void* k_pool, void*
 
 namespace {
 
+// Gives up the plan's workspace for a larger one: freed, or kept (see pa_plan).
+void drop_workspace(pa_plan* plan) {
+    if (!plan->ws) return;
+    if (!plan->keep) {
+        cudaFree(plan->ws);
+        return;
+    }
+    try {
+        plan->retired.push_back(plan->ws);
+    } catch (...) {
+        // No host memory for the list: the block stays allocated for good,
+        // which a graph that uses it survives.
+    }
+}
+
 // Workspace of at least `need` bytes for a windowed call. Memory that a graph
 // captured with this plan may still use stays allocated until pa_free; during
 // a capture nothing can be allocated, and the call is refused instead.
 pa_status grow_workspace(pa_plan* plan, size_t need, cudaStream_t stream) {
+    plan->keep = true;
     if (plan->ws_bytes >= need) return PA_OK;
     cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
     if (cudaStreamIsCapturing(stream, &cap) != cudaSuccess) return PA_ERR_CUDA;
@@ -530,7 +549,7 @@ pa_status decode_impl(const void* q, const int32_t* q_start, int T, int nq, cons
                 const pa_status st = grow_workspace(plan, need, stream);
                 if (st != PA_OK) return st;
             } else if (plan->ws_bytes < need) {
-                if (plan->ws) cudaFree(plan->ws);
+                drop_workspace(plan);
                 plan->ws = nullptr;
                 plan->ws_bytes = 0;
                 if (cudaMalloc(&plan->ws, need) != cudaSuccess) return PA_ERR_CUDA;
@@ -671,7 +690,7 @@ pa_status decode_impl(const void* q, const int32_t* q_start, int T, int nq, cons
         const pa_status st = grow_workspace(plan, need_ws, stream);
         if (st != PA_OK) return st;
     } else if (plan->ws_bytes < need_ws) {
-        if (plan->ws) cudaFree(plan->ws);
+        drop_workspace(plan);
         plan->ws = nullptr;
         plan->ws_bytes = 0;
         if (cudaMalloc(&plan->ws, need_ws) != cudaSuccess) return PA_ERR_CUDA;

@@ -3,6 +3,7 @@
 // only partly filled block of the sequence ("PagedAttention: The Cache Was
 // Storing Nothing" §1 and §2.2). A raw 16-byte-vector copy, bit-exact.
 #include <algorithm>
+#include <atomic>
 
 #include "pa_internal.h"
 #include "pa_ptx.cuh"
@@ -125,7 +126,17 @@ cudaError_t read_append_error(int* err) {
 }  // namespace pa
 
 namespace pa {
+// Looked up once per device: the address stays, and calls that pass no error
+// word of their own are short ones.
 cudaError_t append_error_address(int** p) {
-    return cudaGetSymbolAddress(reinterpret_cast<void**>(p), g_append_error);
+    constexpr int kDevices = 64;
+    static std::atomic<int*> known[kDevices];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < kDevices && (*p = known[dev].load(std::memory_order_relaxed))) return cudaSuccess;
+    e = cudaGetSymbolAddress(reinterpret_cast<void**>(p), g_append_error);
+    if (e == cudaSuccess && dev < kDevices) known[dev].store(*p, std::memory_order_relaxed);
+    return e;
 }
 }  // namespace pa

@@ -359,7 +359,7 @@ pa_status rope_args(RopeArgs* a, const void* q, int64_t q_stride, const void* k,
                  !std::isfinite(rope->amplitude)))
         return PA_ERR_SHAPE;
     if (!aligned16(q) || !aligned16(k) || !aligned16(q_out) || (q_weight && !aligned16(q_weight)) ||
-        (k_weight && !aligned16(k_weight)))
+        (k_weight && !aligned16(k_weight)) || (reinterpret_cast<uintptr_t>(positions) & 3u))
         return PA_ERR_ALIGN;
     a->q = q;
     a->k = k;
@@ -515,7 +515,9 @@ pa_status pa_qk_rope_append(const void* q, int64_t q_stride, const void* k, int6
     if (st != PA_OK) return st;
     const int elem = dtype == PA_F32 ? 4 : 2;
     if (!pa::stride_ok(v_stride, Hkv, D, elem) || num_blocks < 1) return PA_ERR_SHAPE;
-    if (!pa::aligned16(v) || !pa::aligned16(k_pool) || !pa::aligned16(v_pool)) return PA_ERR_ALIGN;
+    if (!pa::aligned16(v) || !pa::aligned16(k_pool) || !pa::aligned16(v_pool) ||
+        (reinterpret_cast<uintptr_t>(slots) & 7u) || (reinterpret_cast<uintptr_t>(device_error) & 3u))
+        return PA_ERR_ALIGN;
     a.v = v;
     a.v_stride = v_stride;
     a.slots = slots;

@@ -193,6 +193,11 @@ extern "C" pa_status pa_step_maps(const int32_t* cache_lens, const int32_t* new_
         num_free < 0 || num_rows < 0)
         return PA_ERR_SHAPE;
     if (static_cast<int64_t>(max_blocks) * block_size > INT32_MAX) return PA_ERR_SHAPE;
+    auto off = [](const void* p, unsigned unit) { return (reinterpret_cast<uintptr_t>(p) & (unit - 1)) != 0; };
+    if (off(cache_lens, 4) || off(new_lens, 4) || off(free_blocks, 4) || off(free_count, 4) ||
+        off(block_tables, 4) || off(seq_lens, 4) || off(q_start, 4) || off(positions, 4) || off(slots, 8) ||
+        off(free_left, 4) || off(device_error, 4))
+        return PA_ERR_ALIGN;
     if (B == 0) return PA_OK;
     // Every block of the grid reads the inputs and block 0 writes these
     // outputs meanwhile: they must be other memory.

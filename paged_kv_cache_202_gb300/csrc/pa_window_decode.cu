@@ -265,10 +265,10 @@ __global__ void __launch_bounds__(32 * kWarpsPerSm, 1)
     }
     __syncthreads();
     auto store = [&](int head, int d, float m, float l, float4 v) {
-        const bool zero = m != m || !(l > 0.f);
-        const float inv = zero ? 0.f : 1.f / l;
+        // The marker m = NaN (not NaN data: maxima pass over it) zeroes the row;
+        // sums that are NaN because a visible key or value is stay so.
+        const float inv = m != m ? 0.f : 1.f / l;
         const size_t o = (row0 + head) * D + d;
-        if (zero) v = make_float4(0.f, 0.f, 0.f, 0.f);  // poisoned sums may be NaN
         if (a.out_bf16)
             *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + o) =
                 make_uint2(pack_bf16x2(v.x * inv, v.y * inv), pack_bf16x2(v.z * inv, v.w * inv));
@@ -350,14 +350,15 @@ cudaError_t window_decode_shape(int64_t segs, int GS, int D, int block_size, int
         // block per SM on the measured chip).
         WindowRoom r{D, block_size, GS, {}};
         auto fn = select_window_decode(D, block_size, NT);
+        // For this call and the later ones of the plan, whatever their shape.
+        cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void*>(fn),
+                                             cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             static_cast<int>(kSmemLimit));
+        if (e != cudaSuccess) return e;
         for (int i = 0; i < 3; ++i) {
             for (int j = 0; j < 4; ++j) {
                 const int W = kWarpsPerSm >> i;
                 const size_t smem = smem_bytes(W, GS, D);
-                cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void*>(fn),
-                                                     cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                     static_cast<int>(smem));
-                if (e != cudaSuccess) return e;
                 if (j == 0) {
                     int n = 0;
                     e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, reinterpret_cast<const void*>(fn), 32 * W, smem);
@@ -425,9 +426,6 @@ cudaError_t launch_window_decode(const CUtensorMap& kmap, const CUtensorMap& vma
     if (blocks > INT32_MAX) return cudaErrorInvalidValue;
     auto fn = select_window_decode(D, block_size, (GS + 7) / 8);
     const size_t smem = smem_bytes(shape.warps, GS, D);
-    const cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void*>(fn),
-                                               cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
-    if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[2];
     cluster_launch(&cfg, attr, shape.cluster, 32 * shape.warps, smem);

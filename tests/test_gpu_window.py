@@ -149,6 +149,20 @@ def test_large_scores_stay_finite():
     p.check(p.run(prefill=True), prefill=True)
 
 
+@pytest.mark.parametrize("prefill", [False, True])
+@pytest.mark.parametrize("where", ["k", "v"])
+def test_visible_values_that_are_not_numbers_show(prefill, where):
+    # A key or value that is NaN and visible is the caller's data: its rows are
+    # NaN, others are not touched.
+    c = Case([300, 400, 90], [1, 1, 1] if prefill else None, Hq=8, Hkv=2, W=60, S=3, seed=2)
+    getattr(c, where)[int(c.table[1, 390 // 16]), 1, 390 % 16] = float("nan")
+    c.upload()
+    out = c.run(prefill=prefill)
+    assert pa.pa_last_device_error(c.plan) == 0
+    assert bool(torch.isnan(out[1, 4:]).all())
+    assert bool(torch.isfinite(out[1, :4]).all()) and bool(torch.isfinite(out[[0, 2]]).all())
+
+
 def test_decode_wrong_lengths_and_entries():
     c = Case([40, 100, 60, 80], W=20, S=4).upload()
     good = c.run()
@@ -311,6 +325,24 @@ def test_graph_replay_outlives_a_growing_plan(prefill):
     torch.cuda.synchronize()
     other.plan = c.plan
     other.check(out, prefill)
+
+
+def test_graph_replay_outlives_plain_calls_that_outgrow_the_plan():
+    c = Case([3000, 2000], [6, 6], W=1000, S=4, seed=1).upload()
+    out = torch.zeros(c.q.shape, dtype=torch.bfloat16, device="cuda")
+    c.run(prefill=True, out=out)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        c.run(prefill=True, out=out)
+    big = Case([2500] * 40, Hq=32, Hkv=8, W=5000, S=0, seed=2).upload()
+    res = torch.empty_like(big.d["q"])
+    pa.pa_decode(big.d["q"], big.d["k"], big.d["v"], big.d["table"], big.d["lens"], big.scale, res, 2500, c.plan)
+    torch.cuda.synchronize()
+    out.zero_()
+    g.replay()
+    torch.cuda.synchronize()
+    c.check(out, True)
 
 
 @pytest.mark.parametrize("prefill", [False, True])

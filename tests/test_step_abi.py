@@ -59,6 +59,9 @@ def _step(lib, **kw):
     (dict(qs=A + 12), pa.PA_ERR_SHAPE),
     (dict(qs=A + 0x100 - 16), pa.PA_ERR_SHAPE),  # q_start has B + 1 entries
     (dict(left=A + 0x200), pa.PA_ERR_SHAPE),
+    (dict(slots=A + 0x604), pa.PA_ERR_ALIGN),
+    (dict(pos=A + 0x502), pa.PA_ERR_ALIGN),
+    (dict(cl=A + 1), pa.PA_ERR_ALIGN),
 ])
 def test_step_maps_refuses_bad_arguments(lib, kw, status):
     assert _step(lib, **kw) == status
@@ -115,6 +118,7 @@ _SHARED = [
     (dict(qo=A + 4), pa.PA_ERR_ALIGN),
     (dict(qw=A + 4), pa.PA_ERR_ALIGN),
     (dict(kw=A + 8), pa.PA_ERR_ALIGN),
+    (dict(pos=A + 2), pa.PA_ERR_ALIGN),
 ]
 _SPECS = {"128": dict(rot_dim=128), "layout": dict(layout=2), "rot": dict(rot_dim=24),
           "amp": dict(amplitude=math.inf)}
@@ -144,6 +148,7 @@ def test_qk_rope_refuses_bad_arguments(lib, kw, status):
     (dict(v=A + 8), pa.PA_ERR_ALIGN),
     (dict(kp=A + 8), pa.PA_ERR_ALIGN),
     (dict(vp=A + 8), pa.PA_ERR_ALIGN),
+    (dict(slots=A + 4), pa.PA_ERR_ALIGN),
 ])
 def test_qk_rope_append_refuses_bad_arguments(lib, kw, status):
     assert _rope(lib, True, **_with_spec(kw)) == status
