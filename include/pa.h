@@ -546,8 +546,9 @@ pa_status pa_decode_noalloc(const void* q, const void* k_pool, const void* v_poo
  * table entry is written as it is and later calls refuse it. seq_lens and
  * q_start must not overlap cache_lens or new_lens, nor free_left free_count
  * (PA_ERR_SHAPE): chained steps alternate between two buffers. Pointers not
- * aligned to their elements return PA_ERR_ALIGN. B = 0 is a no-op. One launch;
- * results do not depend on timing.
+ * aligned to their elements return PA_ERR_ALIGN. B = 0 (the pointers of the
+ * per-request arrays may be NULL) leaves padding only: q_start[0] 0, free_left
+ * free_count, every slot -1. One launch; results do not depend on timing.
  */
 pa_status pa_step_maps(const int32_t* cache_lens, const int32_t* new_lens, int B,
                        const int32_t* free_blocks, int num_free, const int32_t* free_count,

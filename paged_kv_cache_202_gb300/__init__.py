@@ -552,8 +552,6 @@ def pa_step_maps(cache_lens: torch.Tensor, new_lens: torch.Tensor, free_blocks: 
             ("block_tables", block_tables, (B, MB), _I32), ("seq_lens", seq_lens, (B,), _I32),
             ("q_start", q_start, (B + 1,), _I32), ("positions", positions, (T,), _I32),
             ("slots", slots, (T,), _I64), ("free_left", free_left, (1,), _I32)))
-    if B == 0:
-        return
     err = None if device_error is None else _error("pa_step_maps", device_error, dev)
     count = free_count.data_ptr()
     _call("pa_step_maps", lib().pa_step_maps, dev, stream, cache_lens.data_ptr(), new_lens.data_ptr(), B,

@@ -185,8 +185,8 @@ extern "C" pa_status pa_step_maps(const int32_t* cache_lens, const int32_t* new_
                                   int32_t* seq_lens, int32_t* q_start, int32_t* positions,
                                   int64_t* slots, int num_rows, int32_t* free_left,
                                   int* device_error, struct CUstream_st* stream) {
-    if (!cache_lens || !new_lens || !free_blocks || !free_count || !block_tables || !seq_lens ||
-        !q_start || !free_left || (num_rows > 0 && (!positions || !slots)))
+    if (!free_blocks || !free_count || !q_start || !free_left || (num_rows > 0 && (!positions || !slots)) ||
+        (B != 0 && (!cache_lens || !new_lens || !block_tables || !seq_lens)))
         return PA_ERR_NULL;
     if (block_size != 16 && block_size != 32) return PA_ERR_BLOCK_SIZE;
     if (B < 0 || B > pa::kMaxBatch || max_blocks < 1 || num_blocks < 1 || max_seq_len < 1 ||
@@ -198,7 +198,8 @@ extern "C" pa_status pa_step_maps(const int32_t* cache_lens, const int32_t* new_
         off(block_tables, 4) || off(seq_lens, 4) || off(q_start, 4) || off(positions, 4) || off(slots, 8) ||
         off(free_left, 4) || off(device_error, 4))
         return PA_ERR_ALIGN;
-    if (B == 0) return PA_OK;
+    // (No requests: the rows are all padding, and are written as such, so that
+    // no later call takes slots of the step before.)
     // Every block of the grid reads the inputs and block 0 writes these
     // outputs meanwhile: they must be other memory.
     const size_t nb = static_cast<size_t>(B) * 4;

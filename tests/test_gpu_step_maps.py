@@ -29,7 +29,7 @@ class Step:
         cache, new = np.asarray(cache, dtype=np.int32), np.asarray(new, dtype=np.int32)
         self.B, self.bs = len(cache), bs
         had = -(-np.clip(cache, 0, None) // bs)
-        most = int((-(-np.clip(cache.astype(np.int64) + new, 0, 1 << 20) // bs)).max())
+        most = int((-(-np.clip(cache.astype(np.int64) + new, 0, 1 << 20) // bs)).max(initial=0))
         self.MB = MB or most + 1
         fresh = int(np.clip(-(-(cache.astype(np.int64) + new) // bs) - had, 0, 1 << 20).sum())
         self.NB = int(np.minimum(had, self.MB).sum()) + min(fresh, 1 << 20) + spare
@@ -103,6 +103,15 @@ def lens(seed, B, hi_cache, hi_new, idle=0.0):
 ])
 def test_step_maps(bs, cache, new, pad):
     s = Step(cache, new, bs=bs, pad=pad, seed=len(cache)).upload()
+    s.call()
+    assert check(s) == 0
+
+
+@pytest.mark.parametrize("pad", [0, 5, 700])
+def test_no_requests_leave_padding(pad):
+    s = Step([], [], bs=16, pad=pad).upload()
+    for name in ("start", "pos", "slots", "left"):
+        s.o[name].fill_(9)               # a step before
     s.call()
     assert check(s) == 0
 

@@ -67,8 +67,16 @@ def test_step_maps_refuses_bad_arguments(lib, kw, status):
     assert _step(lib, **kw) == status
 
 
-def test_step_maps_of_no_requests_is_a_no_op(lib):
-    assert _step(lib, B=0) == pa.PA_OK
+@pytest.mark.parametrize("kw,status", [
+    (dict(qs=None), pa.PA_ERR_NULL),
+    (dict(slots=None), pa.PA_ERR_NULL),
+    (dict(left=A + 0x200), pa.PA_ERR_SHAPE),
+    (dict(slots=A + 0x604), pa.PA_ERR_ALIGN),
+])
+def test_step_maps_of_no_requests_refuses_bad_arguments(lib, kw, status):
+    a = dict(B=0, cl=None, nl=None, bt=None, sl=None)
+    a.update(kw)
+    assert _step(lib, **a) == status
 
 
 def _spec(**kw):
