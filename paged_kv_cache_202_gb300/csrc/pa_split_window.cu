@@ -1,9 +1,15 @@
 // Split paged decode with a sliding window and sinks (pa_decode_window): the
-// kernels of pa_split.cu over the pages that hold a visible token.
+// kernels of pa_split.cu over the pages that hold a visible token (split_body's
+// WIN), for the few segments so long that a cluster each (pa_window_decode.cu)
+// would leave SMs idle for many rounds.
 //
-// A sequence of L tokens costs min(L, about window + sinks) tokens of K and V
-// whatever its length, so a batch of long contexts runs like a batch of short
-// ones, at the page stream's bandwidth; see split_body's WIN.
+// The visible pages of all sequences form one page stream, which every warp of
+// the grid takes an equal part of; the partial results go through memory and a
+// merge kernel. That second kernel and the finding of a warp's place in the
+// stream cost about 4 us, and for long windows the even split of the stream over
+// all SMs is worth more: one sequence, one kv head, W = 32768, 17.4 us against
+// 27.7 in a cluster of 8 blocks, W = 65536, 22.3 against 46.4. (The calls that
+// come here are chosen in pa_api.cu.)
 #include "pa_split.cuh"
 
 namespace pa {

@@ -5,7 +5,7 @@
 // W + S) tokens, whatever the context's length. So the work is not cut out of
 // one long page stream (pa_split.cuh) but laid out by segment: a segment's
 // visible pages (WindowView) are divided among the warps of one block, or of a
-// cluster of up to 16 blocks where there are few segments, and the warps'
+// cluster of up to 8 blocks where there are few segments, and the warps'
 // partial results (m, l, acc) are merged on the chip -- in shared memory, then
 // across the cluster through distributed shared memory -- with m = max m_i,
 // l = sum l_i 2^(m_i - m), o = sum acc_i 2^(m_i - m) / l ("39 · PagedAttention"
@@ -17,7 +17,10 @@
 // S^T = K Q^T, probabilities as a bf16 pair hi + lo, O^T += V^T P^T, running
 // maximum in the log2 domain; pa_split.cuh's MmaState). Twelve such warps fill an
 // SM's shared memory, in one, two or four blocks. DRAM bounds it for many
-// segments; for few, the latency of one chunk's copies and of the merge.
+// segments, less the last blocks' uneven end: 64 sequences of 8 kv heads, W =
+// 1024, 43.4 us, 6.0 TB/s; 128 of 32, W = 4096, 1145 us, 7.5 TB/s. For few, the
+// latency of a chunk's copies and of the merge bounds it: one sequence of 8 kv
+// heads, W = 8191, 11.8 us, 2.9 TB/s.
 #include "pa_split.cuh"
 
 #include <algorithm>
