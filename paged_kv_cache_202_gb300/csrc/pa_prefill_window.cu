@@ -269,21 +269,17 @@ __device__ __forceinline__ void st_shared_v4(uint32_t addr, uint4 v) {
                  : "memory");
 }
 
-template <int ND>
-__device__ __forceinline__ void write_row(const Args& a, size_t row, const float (&v)[ND], float inv, int d0) {
-    if (a.out_bf16) {
-        uint16_t* o = static_cast<uint16_t*>(a.out) + row * kD + d0;
+// Words j of threads 4 r .. 4 r + 3 become thread 4 r + j's: a 4 x 4 transpose.
+__device__ __forceinline__ void transpose4(uint32_t (&w)[4], int lane) {
 #pragma unroll
-        for (int i = 0; i < ND; i += 8)
-            *reinterpret_cast<uint4*>(o + i) =
-                make_uint4(pack_bf16x2(v[i] * inv, v[i + 1] * inv), pack_bf16x2(v[i + 2] * inv, v[i + 3] * inv),
-                           pack_bf16x2(v[i + 4] * inv, v[i + 5] * inv), pack_bf16x2(v[i + 6] * inv, v[i + 7] * inv));
-    } else {
-        float* o = static_cast<float*>(a.out) + row * kD + d0;
+    for (int bit = 1; bit <= 2; bit <<= 1) {
+        const bool odd = lane & bit;
 #pragma unroll
-        for (int i = 0; i < ND; i += 4)
-            *reinterpret_cast<float4*>(o + i) =
-                make_float4(v[i] * inv, v[i + 1] * inv, v[i + 2] * inv, v[i + 3] * inv);
+        for (int i = 0; i < 2; ++i) {
+            const int j = bit == 1 ? 2 * i : i;   // w[j] and w[j + bit]
+            const uint32_t got = __shfl_xor_sync(0xffffffffu, odd ? w[j] : w[j + bit], bit);
+            (odd ? w[j] : w[j + bit]) = got;
+        }
     }
 }
 
@@ -734,13 +730,43 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc::fence_after_sync();
             const float lt = l + __shfl_xor_sync(0xffffffffu, l, 16);
             const float inv = lt > 0.f ? 1.f / lt : 0.f;
-            const size_t out_row = (static_cast<size_t>(w.it.row) + t * a.Qb + qi) * a.Hq + w.h * a.g + (row - qi * a.g);
+            // Four threads a row, 32 columns of two rows at a time, so that a
+            // store of the warp covers 8 rows by 64 bytes. (Rows as the softmax
+            // holds them, 16 bytes of 32 places a store, kept the stores' path
+            // busy for 4000 cycles an item and all loads behind them waiting.)
+            const int ra = (row & ~15) + (lane >> 2), qa0 = ra / a.g, qa1 = (ra + 8) / a.g;
+            const float inv0 = __shfl_sync(0xffffffffu, inv, lane >> 2);
+            const float inv1 = __shfl_sync(0xffffffffu, inv, (lane >> 2) + 8);
+            const size_t first = (static_cast<size_t>(w.it.row) + t * a.Qb) * a.Hq + w.h * a.g;
+            const size_t at0 = (first + static_cast<size_t>(qa0) * a.Hq + (ra - qa0 * a.g)) * kD;
+            const size_t at1 = (first + static_cast<size_t>(qa1) * a.Hq + (ra + 8 - qa1 * a.g)) * kD;
 #pragma unroll
-            for (int piece = 0; piece < 2; ++piece) {
-                float o[32];
-                tc::ld16x2_32<64>(o_addr + 32 * piece, o);
+            for (int piece = 0; piece < 4; ++piece) {
+                float o[16];
+                tc::ld16x256_4(o_addr + 32 * piece, o);
                 tc::wait_ld();
-                if (qi < nq_t) write_row<32>(a, out_row, o, inv, 64 * half + 32 * piece);
+                if (a.out_bf16) {
+                    uint32_t w0[4], w1[4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        w0[j] = pack_bf16x2(o[4 * j] * inv0, o[4 * j + 1] * inv0);
+                        w1[j] = pack_bf16x2(o[4 * j + 2] * inv1, o[4 * j + 3] * inv1);
+                    }
+                    transpose4(w0, lane);
+                    transpose4(w1, lane);
+                    uint16_t* out = static_cast<uint16_t*>(a.out) + 32 * piece + 8 * (lane & 3);
+                    if (qa0 < nq_t) *reinterpret_cast<uint4*>(out + at0) = make_uint4(w0[0], w0[1], w0[2], w0[3]);
+                    if (qa1 < nq_t) *reinterpret_cast<uint4*>(out + at1) = make_uint4(w1[0], w1[1], w1[2], w1[3]);
+                } else {
+                    float* out = static_cast<float*>(a.out) + 32 * piece + 2 * (lane & 3);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        if (qa0 < nq_t)
+                            *reinterpret_cast<float2*>(out + at0 + 8 * j) = make_float2(o[4 * j] * inv0, o[4 * j + 1] * inv0);
+                        if (qa1 < nq_t)
+                            *reinterpret_cast<float2*>(out + at1 + 8 * j) = make_float2(o[4 * j + 2] * inv1, o[4 * j + 3] * inv1);
+                    }
+                }
             }
             tc::fence_before_sync();
         }

@@ -249,6 +249,22 @@ __device__ __forceinline__ void ld16x2_16(uint32_t taddr, float (&v)[16]) {
     for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
 }
 
+// 32 columns of the 16-lane group at taddr in the 16x256b shape: thread 4 r + c
+// of the warp has columns 8 j + 2 c and 8 j + 2 c + 1 of lane r in v[4 j] and
+// v[4 j + 1], and of lane r + 8 in v[4 j + 2] and v[4 j + 3].
+__device__ __forceinline__ void ld16x256_4(uint32_t taddr, float (&v)[16]) {
+    uint32_t r[16];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+          "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr));
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
+}
+
 // 16 raw words per thread in the 16x32bx2 shape (columns col .. col + 15, or
 // col + SPLIT .. col + SPLIT + 15 for threads 16-31).
 template <int SPLIT>
