@@ -96,8 +96,9 @@ constexpr uint32_t kBarDrain = kBarQEmpty + 16;
 constexpr uint32_t kBarProbe = kBarDrain + 8;              // nothing completes it (wait-expiry probe)
 constexpr uint32_t kSlotTmem = kBarProbe + 8;
 constexpr uint32_t kSlotAbort = kSlotTmem + 4;
-constexpr uint32_t kSmemBytes = 1024 + kOffBar + 256;
-static_assert(kSlotAbort + 4 <= 256, "barrier area");
+constexpr uint32_t kSlotItem = 256;                        // [softmax warp] 16 bytes: its item, while it goes over the chunks
+constexpr uint32_t kSmemBytes = 1024 + kOffBar + kSlotItem + 16 * (kSoftmaxThreads / 32);
+static_assert(kSlotAbort + 4 <= kSlotItem, "barrier area");
 static_assert(kOffK % 1024 == 0 && kOffV % 1024 == 0, "swizzle atoms");
 static_assert(kSmemBytes <= 227 * 1024 && 2 * kSmemBytes > 228 * 1024,
               "one block per SM: it holds all 512 tensor-memory columns");
@@ -131,6 +132,11 @@ struct Args {
     int window, sinks;
     float scale_log2;
     int out_bf16, probe_wait;
+    uint32_t inv_g;           // ceil(2^16 / g)
+
+    // row / g of a row of a tile: exact, as row * (inv_g * g - 2^16) < 2^16 for
+    // row < 144, g <= 128.
+    __device__ __forceinline__ int query_of(int row) const { return static_cast<int>(row * inv_g >> 16); }
 };
 
 // ------------------------------------------------------------------ items
@@ -283,15 +289,34 @@ __device__ __forceinline__ void transpose4(uint32_t (&w)[4], int lane) {
     }
 }
 
+__device__ __forceinline__ uint4 ld_shared_v4(uint32_t addr) {
+    uint4 v;
+    asm volatile("ld.volatile.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "r"(addr)
+                 : "memory");
+    return v;
+}
+
+__device__ __forceinline__ uint32_t ld_shared_u32(uint32_t addr) {
+    uint32_t v;
+    asm volatile("ld.volatile.shared.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+    return v;
+}
+
+__device__ __forceinline__ void st_shared_u32(uint32_t addr, uint32_t v) {
+    asm volatile("st.volatile.shared.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+
 // Bounded wait that also gives up when another role raised the abort flag.
-__device__ __forceinline__ bool wait_role(uint32_t bar, uint32_t parity, volatile int* abort_flag, int* err) {
+__device__ __forceinline__ bool wait_role(uint32_t bar, uint32_t parity, uint32_t abort_flag, int* err) {
     if (mbar_try_wait(bar, parity)) return true;
     const uint64_t t0 = global_timer_ns();
     while (true) {
         if (mbar_try_wait(bar, parity)) return true;
-        if (*abort_flag) return false;
+        if (ld_shared_u32(abort_flag)) return false;
         if (global_timer_ns() - t0 > kWaitLimitNs) {
-            *abort_flag = 1;
+            st_shared_u32(abort_flag, 1);
             atomicOr(err, kErrTimeout);
             return false;
         }
@@ -333,7 +358,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t base = (raw + 1023u) & ~1023u;
     uint8_t* gbase = smem_raw + (base - raw);
     const uint32_t bars = base + kOffBar;
-    volatile int* abort_flag = reinterpret_cast<volatile int*>(gbase + kOffBar + kSlotAbort);
+    const uint32_t abort_flag = bars + kSlotAbort;  // a shared-memory address: one register
 
     if (tid == 0) {
         for (int s = 0; s < kStagesK; ++s) {
@@ -354,7 +379,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         mbar_init(bars + kBarDrain, 1);
         mbar_init(bars + kBarProbe, 1);
-        *abort_flag = 0;
+        st_shared_u32(abort_flag, 0);
         fence_barrier_init();
         prefetch_tensormap(&kmap);
         prefetch_tensormap(&vmap);
@@ -502,7 +527,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // The wait-expiry probe: a bounded wait on a barrier nothing
                 // completes, then the abort every other role follows.
                 mbar_wait_bounded(bars + kBarProbe, 0, kProbeLimitNs);
-                *abort_flag = 1;
+                st_shared_u32(abort_flag, 1);
                 if (lane == 0) atomicOr(a.err, kErrTimeout);
                 ok = false;
             }
@@ -633,11 +658,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int row = 32 * (warp & 3) + 16 * ((warp >> 2) & 1) + (lane & 15);
         const uint32_t lane_base = static_cast<uint32_t>(row & ~15) << 16;
         const uint32_t s_addr = tmem + lane_base + col_s(t);
-        const uint32_t o_addr = tmem + lane_base + col_o(t);
-        const int qi = row / a.g;
+        const uint32_t o_addr = s_addr + (col_o(0) - col_s(0));
+        static_assert(col_o(1) - col_s(1) == col_o(0) - col_s(0), "columns");
+        const int qi = a.query_of(row);
         Walk w(a);
         bool ok = true;
-        int ns = 0, no = 0;   // score tiles taken, outputs read: the barriers' counts
+        uint32_t phase = 0;   // parities: bit 0 of the scores' barrier, bit 1 of the output's
         while (ok && w.next()) {
             const int nq_t = w.it.nq - t * a.Qb;  // queries of this tile
             if (nq_t <= 0) continue;
@@ -648,16 +674,22 @@ __global__ void __launch_bounds__(kThreads, 1)
             // the tile's queries are never stored and need none): from c_hi on
             // those that its first query's position cuts, and c_lo0 .. c_lo1
             // those between the sinks and its last query's window.
-            const int qa = (row & ~15) / a.g, qb = min((row | 15) / a.g, nq_t - 1);
+            const int qa = a.query_of(row & ~15), qb = min(a.query_of(row | 15), nq_t - 1);
             const int c_hi = qa < nq_t ? (pos_t + qa + 1) / kChunk : nc;
             const int c_lo0 = a.sinks / kChunk;
             const int c_lo1 = qa < nq_t && pos_t + qb >= a.window ? (pos_t + qb - a.window) / kChunk : -1;
+            // What only the end of the item needs waits in shared memory: with
+            // it in registers the compiler spilled, to local memory that does
+            // not stay in the 28 KB of L1 left beside the rings.
+            const uint32_t slot = bars + kSlotItem + 16 * warp;
+            if (lane == 0) st_shared_v4(slot, make_uint4(w.id, w.total, w.it.row, nq_t | w.h << 16));
+            __syncwarp();
             float m = -INFINITY, l = 0.f;
             for (int c = 0; c < nc; ++c) {
                 // S_t(c) done; its commit also covers the value product before it.
-                ok = __all_sync(0xffffffffu, wait_role(bars + kBarS + 8 * t, ns & 1, abort_flag, a.err));
+                ok = __all_sync(0xffffffffu, wait_role(bars + kBarS + 8 * t, phase & 1u, abort_flag, a.err));
                 if (!ok) break;
-                ++ns;
+                phase ^= 1u;
                 tc::fence_after_sync();
                 float sv[kChunk / 2];
                 tc::ld16x2_32<64>(s_addr, *reinterpret_cast<float(*)[32]>(sv));
@@ -690,13 +722,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // Rescale this row's half of O_t if its reference max moved.
                 if (c > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
 #pragma unroll
-                    for (int piece = 0; piece < 4; ++piece) {
-                        float o[16];
-                        tc::ld16x2_16<64>(o_addr + 16 * piece, o);
+                    for (int piece = 0; piece < 8; ++piece) {
+                        float o[8];
+                        tc::ld16x2_8<64>(o_addr + 8 * piece, o);
                         tc::wait_ld();
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) o[i] *= alpha;
-                        tc::st16x2_16<64>(o_addr + 16 * piece, o);
+                        for (int i = 0; i < 8; ++i) o[i] *= alpha;
+                        tc::st16x2_8<64>(o_addr + 8 * piece, o);
                     }
                 }
                 const float m_use = m == -INFINITY ? 0.f : m;
@@ -724,9 +756,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!ok) break;
             // The item's rows: O_t normalised, stored by the threads (the query
             // buffer already takes the next item's queries).
-            ok = __all_sync(0xffffffffu, wait_role(bars + kBarO + 8 * t, no & 1, abort_flag, a.err));
+            ok = __all_sync(0xffffffffu, wait_role(bars + kBarO + 8 * t, phase >> 1, abort_flag, a.err));
             if (!ok) break;
-            ++no;
+            phase ^= 2u;
             tc::fence_after_sync();
             const float lt = l + __shfl_xor_sync(0xffffffffu, l, 16);
             const float inv = lt > 0.f ? 1.f / lt : 0.f;
@@ -734,10 +766,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             // store of the warp covers 8 rows by 64 bytes. (Rows as the softmax
             // holds them, 16 bytes of 32 places a store, kept the stores' path
             // busy for 4000 cycles an item and all loads behind them waiting.)
-            const int ra = (row & ~15) + (lane >> 2), qa0 = ra / a.g, qa1 = (ra + 8) / a.g;
+            const uint4 kept = ld_shared_v4(slot);
+            w.id = kept.x;
+            w.total = kept.y;
+            const int nq_end = kept.w & 0xffff;
+            const int ra = (row & ~15) + (lane >> 2), qa0 = a.query_of(ra), qa1 = a.query_of(ra + 8);
             const float inv0 = __shfl_sync(0xffffffffu, inv, lane >> 2);
             const float inv1 = __shfl_sync(0xffffffffu, inv, (lane >> 2) + 8);
-            const size_t first = (static_cast<size_t>(w.it.row) + t * a.Qb) * a.Hq + w.h * a.g;
+            const size_t first = (static_cast<size_t>(kept.z) + t * a.Qb) * a.Hq + (kept.w >> 16) * a.g;
             const size_t at0 = (first + static_cast<size_t>(qa0) * a.Hq + (ra - qa0 * a.g)) * kD;
             const size_t at1 = (first + static_cast<size_t>(qa1) * a.Hq + (ra + 8 - qa1 * a.g)) * kD;
 #pragma unroll
@@ -755,15 +791,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                     transpose4(w0, lane);
                     transpose4(w1, lane);
                     uint16_t* out = static_cast<uint16_t*>(a.out) + 32 * piece + 8 * (lane & 3);
-                    if (qa0 < nq_t) *reinterpret_cast<uint4*>(out + at0) = make_uint4(w0[0], w0[1], w0[2], w0[3]);
-                    if (qa1 < nq_t) *reinterpret_cast<uint4*>(out + at1) = make_uint4(w1[0], w1[1], w1[2], w1[3]);
+                    if (qa0 < nq_end) *reinterpret_cast<uint4*>(out + at0) = make_uint4(w0[0], w0[1], w0[2], w0[3]);
+                    if (qa1 < nq_end) *reinterpret_cast<uint4*>(out + at1) = make_uint4(w1[0], w1[1], w1[2], w1[3]);
                 } else {
                     float* out = static_cast<float*>(a.out) + 32 * piece + 2 * (lane & 3);
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
-                        if (qa0 < nq_t)
+                        if (qa0 < nq_end)
                             *reinterpret_cast<float2*>(out + at0 + 8 * j) = make_float2(o[4 * j] * inv0, o[4 * j + 1] * inv0);
-                        if (qa1 < nq_t)
+                        if (qa1 < nq_end)
                             *reinterpret_cast<float2*>(out + at1 + 8 * j) = make_float2(o[4 * j + 2] * inv1, o[4 * j + 3] * inv1);
                     }
                 }
@@ -809,6 +845,7 @@ cudaError_t launch_prefill_window(const CUtensorMap& kmap, const CUtensorMap& vm
     a.Hkv = Hkv;
     a.g = Hq / Hkv;
     a.Qb = kRows / a.g;
+    a.inv_g = (65536u + a.g - 1) / a.g;
     a.num_q = num_q;
     a.max_q = max_q;
     a.max_items = static_cast<int>(std::min<int64_t>(items_bound(B, Hq, Hkv, num_q), INT32_MAX / Hkv - num_sms));

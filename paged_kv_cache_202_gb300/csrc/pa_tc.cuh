@@ -233,20 +233,25 @@ __device__ __forceinline__ void st16x2_32(uint32_t taddr, const float (&v)[32]) 
         : "memory");
 }
 
-// 16 columns a thread in the same shape (columns col .. col + 15, or col + SPLIT
-// .. col + SPLIT + 15 for threads 16-31).
+// 8 floats per thread in the 16x32bx2 shape, loaded and stored.
 template <int SPLIT>
-__device__ __forceinline__ void ld16x2_16(uint32_t taddr, float (&v)[16]) {
-    uint32_t r[16];
-    asm volatile(
-        "tcgen05.ld.sync.aligned.16x32bx2.x16.b32 "
-        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16], %17;"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
-          "=r"(r[14]), "=r"(r[15])
-        : "r"(taddr), "n"(SPLIT));
+__device__ __forceinline__ void ld16x2_8(uint32_t taddr, float (&v)[8]) {
+    uint32_t r[8];
+    asm volatile("tcgen05.ld.sync.aligned.16x32bx2.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8], %9;"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(taddr), "n"(SPLIT));
 #pragma unroll
-    for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
+    for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+template <int SPLIT>
+__device__ __forceinline__ void st16x2_8(uint32_t taddr, const float (&v)[8]) {
+    uint32_t r[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) r[i] = __float_as_uint(v[i]);
+    asm volatile("tcgen05.st.sync.aligned.16x32bx2.x8.b32 [%0], %9, {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr),
+                 "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "n"(SPLIT)
+                 : "memory");
 }
 
 // 32 columns of the 16-lane group at taddr in the 16x256b shape: thread 4 r + c
@@ -276,14 +281,6 @@ __device__ __forceinline__ void st16x2_16u(uint32_t taddr, const uint32_t (&r)[1
         "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]),
         "n"(SPLIT)
         : "memory");
-}
-
-template <int SPLIT>
-__device__ __forceinline__ void st16x2_16(uint32_t taddr, const float (&v)[16]) {
-    uint32_t r[16];
-#pragma unroll
-    for (int i = 0; i < 16; ++i) r[i] = __float_as_uint(v[i]);
-    st16x2_16u<SPLIT>(taddr, r);
 }
 
 __device__ __forceinline__ void wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
