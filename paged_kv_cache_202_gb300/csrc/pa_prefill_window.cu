@@ -58,8 +58,8 @@ namespace {
 constexpr int kRows = 128;      // M: query rows per tile
 constexpr int kChunk = 128;     // tokens per K/V chunk
 constexpr int kD = 128;         // head dimension
-constexpr int kStagesK = 2;     // K ring depth
-constexpr int kStagesV = 3;     // V ring depth (the value product waits on V last)
+constexpr int kStagesK = 3;     // K ring depth
+constexpr int kStagesV = 2;     // V ring depth
 constexpr int kTileThreads = 2 * kRows;             // softmax threads of a tile: two per row
 constexpr int kSoftmaxThreads = 2 * kTileThreads;
 constexpr int kWarpLoad = kSoftmaxThreads / 32;     // warp 16: Q and K copies
