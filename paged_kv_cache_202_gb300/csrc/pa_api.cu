@@ -401,18 +401,24 @@ pa_status grow_workspace(pa_plan* plan, size_t need, cudaStream_t stream) {
     return PA_OK;
 }
 
-// Which kernel a windowed multi-query call runs: the one-tile kernel where every
-// sequence fits one tile (the other's second tile would be empty: 64 sequences
-// of 40 queries, one head a group, W = 4096: 194 against 221 us) or where its
-// tiles do not fill the SMs once, so that its key split can (512 queries, 128
-// tiles, W = 1024: 19 against 27 us); the persistent kernel over pairs of tiles
-// otherwise (1024 queries, 256 tiles: 28 against 36 us; 16 x 256 queries, 1024
-// tiles, W = 2048: 143 against 184 us).
-bool window_items(int B, int Hq, int Hkv, int64_t nq, int num_sms) {
+// Which kernel a windowed multi-query call runs. The persistent kernel over
+// pairs of tiles saves the 3 us that a block takes to fill and drain its
+// pipeline, and the second copy of a pair's keys and values; it costs the item
+// list, 4 us, and has no key split. So, with sequences of several tiles, it runs
+// as soon as the tiles fill the SMs once (9 x 40 queries, 144 tiles, W = 2048:
+// 35 against 28 us; 14 x 40, 224 tiles: 39 against 52; 16 x 256, 1024 tiles: 111
+// against 184). With one tile a sequence its second tile is empty, and what it
+// saves shows over several rounds of blocks and short windows only (1280 tiles
+// of 6 queries, 9 rounds, W = 256: 71 against 99 us, W = 1024: 148 against 165,
+// W = 4096: 454 against 445; 304 tiles, 2 rounds, W = 256: 23 against 20).
+bool window_items(int B, int Hq, int Hkv, int64_t nq, int vis_len, int num_sms) {
     const int qb = 128 / (Hq / Hkv);
     const int force = pa::prefill_kernel_choice();  // a test may pin either kernel
     if (force != PA_PREFILL_AUTO) return force == PA_PREFILL_TWO_TILE;
-    return nq > qb && (nq + qb - 1) / qb * static_cast<int64_t>(Hkv) * B > num_sms;
+    const int64_t tiles = (nq + qb - 1) / qb * static_cast<int64_t>(Hkv) * B;
+    const int64_t rounds = (tiles + num_sms - 1) / num_sms;
+    if (nq > qb) return tiles > num_sms;
+    return rounds >= 4 && 2 * rounds >= (vis_len + 127) / 128;
 }
 
 // The decode of pa_decode, with q_start != null (T query rows, at most nq per
@@ -524,7 +530,7 @@ pa_status decode_impl(const void* q, const int32_t* q_start, int T, int nq, cons
         // workspace after its first 64 bytes, which hold the split decode's
         // counters (zero between calls, left untouched here).
         const int64_t nqq = std::min<int64_t>(nq, T);
-        if (window > 0 && window_items(B, Hq, Hkv, nqq, plan->num_sms)) {
+        if (window > 0 && window_items(B, Hq, Hkv, nqq, vis_len, plan->num_sms)) {
             const size_t need = 64 + pa::prefill_window_bytes(B, Hq, Hkv, T);
             const pa_status st = grow_workspace(plan, need, stream);
             if (st != PA_OK) return st;
