@@ -39,6 +39,16 @@
 // last tiles first, lengths and table entries validated once for all heads. Items
 // go to blocks in turn.
 //
+// What bounds it: the tensor cores are busy 68 % of the time. A tile's chain (its
+// value products 512 cycles, its next score products 512, its softmax 1200, the
+// hand-overs) is 2500 cycles a chunk against 2048 of products for both tiles, and
+// an item's end costs 2500 to 5000 more: 16384 rows of W = 4096 612 us, 1594
+// TFLOP/s (in passes apart; 690 us back to back at the power cap); 16 x 256 rows
+// of W = 2048 103 us, 1078 TFLOP/s (3.4 rounds of items in four); 4 x 4096 rows of
+// W = 128 89 us. So the code beside the softmax's loop counts: with its spills to
+// local memory, which does not stay in what the rings leave of L1, and O stored
+// by rows, the first took 691 us and the last 125.
+//
 // Every mbarrier wait is bounded. A role that gives up raises a shared abort
 // flag (and PA_DEVERR_TIMEOUT); the others see it in their own waits. Before
 // the block leaves, the copy warps wait (bounded) for their copies in flight,
@@ -721,7 +731,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 // Rescale this row's half of O_t if its reference max moved.
                 if (c > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
-#pragma unroll
+#pragma unroll 1  // rare, and short code keeps the rest in the instruction cache
                     for (int piece = 0; piece < 8; ++piece) {
                         float o[8];
                         tc::ld16x2_8<64>(o_addr + 8 * piece, o);
