@@ -406,7 +406,7 @@ pa_status grow_workspace(pa_plan* plan, size_t need, cudaStream_t stream) {
 // pipeline, and the second copy of a pair's keys and values; it costs the item
 // list, 4 us, and has no key split. So, with sequences of several tiles, it runs
 // as soon as the tiles fill the SMs once (9 x 40 queries, 144 tiles, W = 2048:
-// 35 against 28 us; 14 x 40, 224 tiles: 39 against 52; 16 x 256, 1024 tiles: 111
+// 35 against 28 us; 14 x 40, 224 tiles: 39 against 52; 16 x 256, 1024 tiles: 103
 // against 184). With one tile a sequence its second tile is empty, and what it
 // saves shows over several rounds of blocks and short windows only (1280 tiles
 // of 6 queries, 9 rounds, W = 256: 71 against 99 us, W = 1024: 148 against 165,

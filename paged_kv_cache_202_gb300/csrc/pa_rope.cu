@@ -22,7 +22,7 @@
 // row, so a thread's 8 sines and cosines serve all its heads (few rows: several
 // warps share a row). The bytes bound it -- every element is read once and
 // written once: 16421 rows of 32 + 8 heads 51.9 us, 6.48 TB/s -- until the norms
-// come in, whose arithmetic fills 60 % of the issue slots: 32768 rows of 32 + 8 +
+// come in, whose arithmetic fills 47 % of the issue slots: 32768 rows of 32 + 8 +
 // 8 heads 135 us, 5.96 TB/s (126 us without norms). Few rows are bound by the
 // launch and one round trip: 64 rows 2.4 us, 2.8 us with the cache write.
 // A ring of rows in shared memory filled by bulk copies, instead of loads held in
