@@ -142,11 +142,7 @@ struct Args {
     int window, sinks;
     float scale_log2;
     int out_bf16, probe_wait;
-    uint32_t inv_g;           // ceil(2^16 / g)
-
-    // row / g of a row of a tile: exact, as row * (inv_g * g - 2^16) < 2^16 for
-    // row < 144, g <= 128.
-    __device__ __forceinline__ int query_of(int row) const { return static_cast<int>(row * inv_g >> 16); }
+    int lg;                   // g = 2^lg (it divides 128)
 };
 
 // ------------------------------------------------------------------ items
@@ -670,7 +666,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t s_addr = tmem + lane_base + col_s(t);
         const uint32_t o_addr = s_addr + (col_o(0) - col_s(0));
         static_assert(col_o(1) - col_s(1) == col_o(0) - col_s(0), "columns");
-        const int qi = a.query_of(row);
+        const int qi = row >> a.lg;
         Walk w(a);
         bool ok = true;
         uint32_t phase = 0;   // parities: bit 0 of the scores' barrier, bit 1 of the output's
@@ -684,7 +680,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             // the tile's queries are never stored and need none): from c_hi on
             // those that its first query's position cuts, and c_lo0 .. c_lo1
             // those between the sinks and its last query's window.
-            const int qa = a.query_of(row & ~15), qb = min(a.query_of(row | 15), nq_t - 1);
+            const int qa = ((row & ~15) >> a.lg), qb = min((row | 15) >> a.lg, nq_t - 1);
             const int c_hi = qa < nq_t ? (pos_t + qa + 1) / kChunk : nc;
             const int c_lo0 = a.sinks / kChunk;
             const int c_lo1 = qa < nq_t && pos_t + qb >= a.window ? (pos_t + qb - a.window) / kChunk : -1;
@@ -780,12 +776,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             w.id = kept.x;
             w.total = kept.y;
             const int nq_end = kept.w & 0xffff;
-            const int ra = (row & ~15) + (lane >> 2), qa0 = a.query_of(ra), qa1 = a.query_of(ra + 8);
+            const int ra = (row & ~15) + (lane >> 2), qa0 = ra >> a.lg, qa1 = (ra + 8) >> a.lg;
             const float inv0 = __shfl_sync(0xffffffffu, inv, lane >> 2);
             const float inv1 = __shfl_sync(0xffffffffu, inv, (lane >> 2) + 8);
             const size_t first = (static_cast<size_t>(kept.z) + t * a.Qb) * a.Hq + (kept.w >> 16) * a.g;
-            const size_t at0 = (first + static_cast<size_t>(qa0) * a.Hq + (ra - qa0 * a.g)) * kD;
-            const size_t at1 = (first + static_cast<size_t>(qa1) * a.Hq + (ra + 8 - qa1 * a.g)) * kD;
+            const size_t at0 = (first + static_cast<size_t>(qa0) * a.Hq + (ra & (a.g - 1))) * kD;
+            const size_t at1 = (first + static_cast<size_t>(qa1) * a.Hq + ((ra + 8) & (a.g - 1))) * kD;
 #pragma unroll
             for (int piece = 0; piece < 4; ++piece) {
                 float o[16];
@@ -855,7 +851,8 @@ cudaError_t launch_prefill_window(const CUtensorMap& kmap, const CUtensorMap& vm
     a.Hkv = Hkv;
     a.g = Hq / Hkv;
     a.Qb = kRows / a.g;
-    a.inv_g = (65536u + a.g - 1) / a.g;
+    a.lg = 0;
+    while (1 << a.lg < a.g) ++a.lg;
     a.num_q = num_q;
     a.max_q = max_q;
     a.max_items = static_cast<int>(std::min<int64_t>(items_bound(B, Hq, Hkv, num_q), INT32_MAX / Hkv - num_sms));
