@@ -531,7 +531,7 @@ pa_status decode_impl(const void* q, const int32_t* q_start, int T, int nq, cons
         // counters (zero between calls, left untouched here).
         const int64_t nqq = std::min<int64_t>(nq, T);
         if (window > 0 && window_items(B, Hq, Hkv, nqq, vis_len, plan->num_sms)) {
-            const size_t need = 64 + pa::prefill_window_bytes(B, Hq, Hkv, T);
+            const size_t need = 64 + pa::prefill_window_bytes(B, Hq, Hkv, T, vis_len, plan->num_sms);
             const pa_status st = grow_workspace(plan, need, stream);
             if (st != PA_OK) return st;
             plan->cnt_clean = std::min(plan->cnt_clean, plan->ws_bytes - need);
@@ -539,8 +539,8 @@ pa_status decode_impl(const void* q, const int32_t* q_start, int T, int nq, cons
             const cudaError_t e = pa::launch_prefill_window(
                 kmap, vmap, q, T, q_start, block_tables, seq_lens, out, plan->err, B, Hq, Hkv,
                 max_blocks, num_blocks, max_seq_len, nq, scale_log2, window, sinks,
-                out_dtype == PA_BF16, block_size, plan->num_sms, static_cast<char*>(plan->ws) + 64,
-                stream);
+                out_dtype == PA_BF16, block_size, vis_len, plan->num_sms,
+                static_cast<char*>(plan->ws) + 64, stream);
             if (plan->ev_stop) cudaEventRecord(plan->ev_stop, stream);
             plan->last_path = PA_PATH_PREFILL;
             plan->last_blocks = 0;

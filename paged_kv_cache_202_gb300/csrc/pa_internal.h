@@ -287,8 +287,8 @@ cudaError_t launch_prefill_window(const CUtensorMap& kmap, const CUtensorMap& vm
                                   const int32_t* seq_lens, void* out, int* err, int B, int Hq, int Hkv,
                                   int max_blocks, int num_blocks, int max_seq_len, int max_q,
                                   float scale_log2, int window, int sinks, int out_bf16, int block_size,
-                                  int num_sms, void* ws, cudaStream_t stream);
-size_t prefill_window_bytes(int B, int Hq, int Hkv, int num_q);
+                                  int vis_len, int num_sms, void* ws, cudaStream_t stream);
+size_t prefill_window_bytes(int B, int Hq, int Hkv, int num_q, int vis_len, int num_sms);
 // pa_decode_window's kernel (pa_window_decode.cu). The clusters of each size (1,
 // 2, 4, 8 blocks) that the device holds at a time with one, two or four blocks
 // an SM, kept in the plan; the warps per block and blocks per segment of a call.

@@ -37,7 +37,12 @@
 //
 // The items come from window_items_kernel: sequences in order of length, their
 // last tiles first, lengths and table entries validated once for all heads. Items
-// go to blocks in turn.
+// go to blocks in turn. With few turns of long items, and at most half of the
+// blocks at work in the last, a second build of the kernel (PARTS) cuts the last
+// turn's items into parts by keys, one block a part: every warp leaves its 16
+// rows' (m, l, O) of the part in memory and counts up, and the last to arrive
+// merges them in the order of the parts, with m = max m_i, l = sum l_i 2^(m_i -
+// m), o = sum O_i 2^(m_i - m) / l. No warp waits for another.
 //
 // What bounds it: the tensor cores are busy 68 % of the time. A tile's chain (its
 // value products 512 cycles, its next score products 512, its softmax 1200, the
@@ -83,6 +88,12 @@ constexpr uint32_t kTmemCols = 512;
 __host__ __device__ constexpr uint32_t col_s(int t) { return 128u * t; }
 __host__ __device__ constexpr uint32_t col_o(int t) { return 256u + 128u * t; }
 constexpr float kRescaleLog2 = 8.f;
+constexpr int kMaxParts = 4;       // of an item of the last turn
+constexpr int kMinPartChunks = 8;  // chunks a part
+constexpr int kWarpsPerItem = kSoftmaxThreads / 32;
+// A part's partial results: O [tile x 8 + warp][32 columns][register / 4][lane],
+// as the warps read it for the output, then (m, l) of every row.
+constexpr size_t kPartFloats = 2 * kRows * (kD + 2);
 
 // Shared-memory layout (byte offsets from a 1024-aligned base).
 constexpr uint32_t kTileQ = 32768;                    // 2 halves x 128 rows x 128 B
@@ -106,8 +117,8 @@ constexpr uint32_t kBarDrain = kBarQEmpty + 16;
 constexpr uint32_t kBarProbe = kBarDrain + 8;              // nothing completes it (wait-expiry probe)
 constexpr uint32_t kSlotTmem = kBarProbe + 8;
 constexpr uint32_t kSlotAbort = kSlotTmem + 4;
-constexpr uint32_t kSlotItem = 256;                        // [softmax warp] 16 bytes: its item, while it goes over the chunks
-constexpr uint32_t kSmemBytes = 1024 + kOffBar + kSlotItem + 16 * (kSoftmaxThreads / 32);
+constexpr uint32_t kSlotItem = 256;                        // [softmax warp] 32 bytes: its item, while it goes over the chunks
+constexpr uint32_t kSmemBytes = 1024 + kOffBar + kSlotItem + 32 * (kSoftmaxThreads / 32);
 static_assert(kSlotAbort + 4 <= kSlotItem, "barrier area");
 static_assert(kOffK % 1024 == 0 && kOffV % 1024 == 0, "swizzle atoms");
 static_assert(kSmemBytes <= 227 * 1024 && 2 * kSmemBytes > 228 * 1024,
@@ -134,6 +145,8 @@ struct Args {
     const int32_t* seq_lens;
     Item* items;
     int* num_items;
+    int* arrived;             // [blocks][kWarpsPerItem] parts done, of the item whose first part is the block's
+    float* parts;             // [blocks][kPartFloats]; null: no parts
     void* out;
     int* err;
     int B, Hq, Hkv, g, Qb;    // Qb = queries per tile = 128 / g
@@ -142,6 +155,7 @@ struct Args {
     int window, sinks;
     float scale_log2;
     int out_bf16, probe_wait;
+    int num_sms;
     int lg;                   // g = 2^lg (it divides 128)
 };
 
@@ -171,6 +185,9 @@ __global__ void __launch_bounds__(kItemThreads) window_items_kernel(const Args a
     griddep_launch_dependents();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int limit = min(a.max_seq_len, a.max_blocks * BS);
+    if (a.parts)
+        for (int i = blockIdx.x * kItemThreads + tid; i < a.num_sms * kWarpsPerItem; i += gridDim.x * kItemThreads)
+            a.arrived[i] = 0;
     // The items of sequence b: -1 if its lengths are wrong.
     auto count = [&](int b) {
         const int64_t qs = a.q_start[b], n = static_cast<int64_t>(a.q_start[b + 1]) - qs;
@@ -329,32 +346,123 @@ __device__ __forceinline__ bool wait_role(uint32_t bar, uint32_t parity, uint32_
     }
 }
 
-// This block's items in order: index id of the list x kv heads (the heads of an
-// item next to each other, so that running blocks share K/V pages in L2).
+// The end of an item's part for the 16 rows of a warp: their (m, l, O) go to
+// memory. True for the warp that is the last of the item's parts to do so: with
+// the weights 2^(m_i - max m) of row lane & 15 in the parts, in their order, and
+// the reciprocal of its sum. No warp waits for another.
+__device__ __forceinline__ bool leave_part(const Args& a, uint32_t o_addr, float m, float lt, int part,
+                                           float (&weight)[kMaxParts], float* inv) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    float* mine = a.parts + blockIdx.x * kPartFloats;
+#pragma unroll
+    for (int piece = 0; piece < 4; ++piece) {
+        float o[16];
+        tc::ld16x256_4(o_addr + 32 * piece, o);
+        tc::wait_ld();
+        float4* to = reinterpret_cast<float4*>(mine) + (warp * 4 + piece) * 128 + lane;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) __stcg(to + 32 * k, make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]));
+    }
+    tc::fence_before_sync();
+    const size_t ml = 2 * kRows * kD + 2 * (warp * 16 + (lane & 15));
+    if (lane < 16) __stcg(reinterpret_cast<float2*>(mine + ml), make_float2(m, lt));
+    __threadfence();
+    __syncwarp();
+    const int parts = part & 7;
+    int before = 0;
+    if (lane == 0) before = atomicAdd(a.arrived + (part >> 3) * kWarpsPerItem + warp, 1);
+    if (__shfl_sync(0xffffffffu, before, 0) != parts - 1) return false;
+    __threadfence();
+    const float* first = a.parts + (part >> 3) * kPartFloats + ml;
+    float l[kMaxParts], mm = -INFINITY, lm = 0.f;
+#pragma unroll
+    for (int i = 0; i < kMaxParts; ++i) {
+        const float2 v = i < parts ? __ldcg(reinterpret_cast<const float2*>(first + i * kPartFloats))
+                                   : make_float2(-INFINITY, 0.f);
+        weight[i] = v.x;
+        l[i] = v.y;
+    }
+#pragma unroll
+    for (int i = 0; i < kMaxParts; ++i) mm = fmaxf(mm, weight[i]);
+    if (mm == -INFINITY) mm = 0.f;   // a row that sees nothing: its sums are 0
+#pragma unroll
+    for (int i = 0; i < kMaxParts; ++i) {
+        weight[i] = fast_exp2(weight[i] - mm);
+        lm += l[i] * weight[i];
+    }
+    *inv = lm > 0.f ? 1.f / lm : 0.f;
+    return true;
+}
+
+// 32 columns of the merged O, as tc::ld16x256_4 gives them.
+__device__ __forceinline__ void merge_parts(const Args& a, int part, int piece, const float (&weight)[kMaxParts],
+                                            float (&o)[16]) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const float4* from = reinterpret_cast<const float4*>(a.parts + (part >> 3) * kPartFloats) + (warp * 4 + piece) * 128 + lane;
+#pragma unroll
+    for (int k = 0; k < 16; ++k) o[k] = 0.f;
+#pragma unroll
+    for (int i = 0; i < kMaxParts; ++i) {
+        if (i >= (part & 7)) break;
+        const float w0 = __shfl_sync(0xffffffffu, weight[i], lane >> 2);
+        const float w1 = __shfl_sync(0xffffffffu, weight[i], (lane >> 2) + 8);
+        float4 v[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) v[k] = __ldcg(from + i * (kPartFloats / 4) + 32 * k);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            o[4 * k] += w0 * v[k].x;
+            o[4 * k + 1] += w0 * v[k].y;
+            o[4 * k + 2] += w1 * v[k].z;
+            o[4 * k + 3] += w1 * v[k].w;
+        }
+    }
+}
+
+// This block's items in order: entry `turn * grid + block` of the list x kv heads
+// (the heads of an item next to each other, so that running blocks share K/V
+// pages in L2). PARTS: the items of a last, incomplete turn are cut into up to
+// kMaxParts parts where the blocks suffice, block u * cut + i has part i of the
+// turn's item u.
+template <bool PARTS>
 struct Walk {
     const Args& a;
-    int id, total;
+    int total, turn;
     Item it;
-    int h, nc;  // kv head, chunks of the item
+    int h, c0, nc;  // kv head, first chunk, chunks
+    int part;       // 0: the whole item; else its number of parts, and 8 x the block of the first
     __device__ __forceinline__ Walk(const Args& args)
-        : a(args), id(static_cast<int>(blockIdx.x) - static_cast<int>(gridDim.x)), total(*args.num_items * args.Hkv) {}
+        : a(args), total(*args.num_items * args.Hkv), turn(-1), c0(0), part(0) {}
     __device__ __forceinline__ bool next() {
+        const int grid = gridDim.x;
         while (true) {
-            if (total - id <= static_cast<int>(gridDim.x)) return false;
-            id += gridDim.x;
+            ++turn;
+            const int left = total - turn * grid;   // from this turn on
+            const int cut = PARTS && left > 0 && left < grid ? min(kMaxParts, grid / left) : 1;
+            const int u = PARTS ? static_cast<int>(blockIdx.x) / cut : static_cast<int>(blockIdx.x);
+            if (u >= left) return false;
+            const int id = turn * grid + u;
             const int e = id / a.Hkv;
             const int4* p = reinterpret_cast<const int4*>(a.items + e);
-            const int4 u = p[0], w = p[1];
-            if (u.z == 0) continue;
-            it = Item{u.x, u.y, u.z, u.w, w.x, w.y, w.z, 0};
+            const int4 x = p[0], w = p[1];
+            if (x.z == 0) continue;
+            it = Item{x.x, x.y, x.z, x.w, w.x, w.y, w.z, 0};
             h = id - e * a.Hkv;
             nc = (it.len + kChunk - 1) / kChunk;
+            if (PARTS) c0 = 0, part = 0;
+            if (PARTS && cut > 1) {
+                const int per = max(kMinPartChunks, (nc + cut - 1) / cut), parts = (nc + per - 1) / per;
+                c0 = (blockIdx.x - u * cut) * per;
+                if (parts > 1) part = parts + 8 * u * cut;
+                nc = min(per, nc - c0);
+                if (nc <= 0) continue;
+            }
             return true;
         }
     }
 };
 
-template <int BS>
+template <int BS, bool PARTS>
 __global__ void __launch_bounds__(kThreads, 1)
     window_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                   const __grid_constant__ CUtensorMap qmap, const __grid_constant__ Args a) {
@@ -422,7 +530,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             };
             // K/V pages of an item are read again for the item's neighbours:
             // no eviction hint, unlike the kernels that read a page once.
-            Walk w(a);
+            Walk<PARTS> w(a);
             int s = 0;                 // ring stage
             uint32_t parity = 1;       // of its last release: a fresh stage counts as released
             int issued = 0;            // chunks in the ring, at most nst
@@ -433,9 +541,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int32_t* table = a.tables + static_cast<size_t>(w.it.b) * a.max_blocks;
                 const int nb = __shfl_sync(0xffffffffu, (w.it.len + BS - 1) / BS, 0);
                 const int nc = __shfl_sync(0xffffffffu, w.nc, 0), h = __shfl_sync(0xffffffffu, w.h, 0);
+                const int c0 = PARTS ? __shfl_sync(0xffffffffu, w.c0, 0) : 0;
                 // Lane j: the block of page j of chunk c, one chunk ahead.
                 auto entries = [&](int c) {
-                    const int p = c * kPages + lane;
+                    const int p = (c0 + c) * kPages + lane;
                     return lane < kPages && p < nb ? table[p < sink_pages ? p : p + w.it.skip] : 0;
                 };
                 int pg = entries(0);
@@ -443,7 +552,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const int pg_next = c + 1 < nc ? entries(c + 1) : 0;
                     ok = wait(empty + 8 * s, parity);
                     if (!ok) break;
-                    const int np = min(kPages, nb - c * kPages);
+                    const int np = min(kPages, nb - (c0 + c) * kPages);
                     const uint32_t bar = full + 8 * s, stage = ring + s * kStageKV;
                     if (one) mbar_arrive_expect_tx(bar, static_cast<uint32_t>(np) * BS * kD * 2);
                     __syncwarp();
@@ -537,7 +646,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (lane == 0) atomicOr(a.err, kErrTimeout);
                 ok = false;
             }
-            Walk w(a);
+            Walk<PARTS> w(a);
             // Ring stages and parities of the chunk whose value products come
             // next, and of the chunk whose score products do; parities of P and
             // of the query tiles.
@@ -625,14 +734,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             // S_0 of the chunk, so never for a later one. The wait for V is
             // unambiguous: S_0 of this step was issued after the value product
             // of the step before, which waited for that step's V.
-            Walk w(a);
+            Walk<PARTS> w(a);
             int step = 0;
             bool ok = true;
             while (ok && w.next()) {
                 for (int c = 0; c < w.nc; ++c, ++step) {
                     ok = __all_sync(0xffffffffu, wait_role(bars + kBarS, step & 1, abort_flag, a.err));
                     if (!ok) break;
-                    const int v0 = c * kChunk;
+                    const int v0 = (w.c0 + c) * kChunk;
                     const int h0 = max(0, a.sinks - v0), h1 = min(kChunk, w.it.lo - v0);
                     const int valid = min(kChunk, w.it.len - v0);
                     if (valid < kChunk || h0 < h1) {
@@ -667,14 +776,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t o_addr = s_addr + (col_o(0) - col_s(0));
         static_assert(col_o(1) - col_s(1) == col_o(0) - col_s(0), "columns");
         const int qi = row >> a.lg;
-        Walk w(a);
+        Walk<PARTS> w(a);
         bool ok = true;
         uint32_t phase = 0;   // parities: bit 0 of the scores' barrier, bit 1 of the output's
         while (ok && w.next()) {
             const int nq_t = w.it.nq - t * a.Qb;  // queries of this tile
             if (nq_t <= 0) continue;
             const int nc = w.nc;
-            const int pos_t = w.it.pos + t * a.Qb - w.it.skip * BS;  // last index the tile's first query sees
+            // Indices count from the part's first chunk on. The last that the
+            // tile's first query sees:
+            const int pos_t = w.it.pos + t * a.Qb - w.it.skip * BS - w.c0 * kChunk;
             const int pos_r = pos_t + qi;                            // ... and this row's
             // The chunks that need a mask for some query of this warp (rows past
             // the tile's queries are never stored and need none): from c_hi on
@@ -682,13 +793,17 @@ __global__ void __launch_bounds__(kThreads, 1)
             // those between the sinks and its last query's window.
             const int qa = ((row & ~15) >> a.lg), qb = min((row | 15) >> a.lg, nq_t - 1);
             const int c_hi = qa < nq_t ? (pos_t + qa + 1) / kChunk : nc;
-            const int c_lo0 = a.sinks / kChunk;
+            const int sinks = a.sinks - w.c0 * kChunk;
+            const int c_lo0 = sinks / kChunk;
             const int c_lo1 = qa < nq_t && pos_t + qb >= a.window ? (pos_t + qb - a.window) / kChunk : -1;
             // What only the end of the item needs waits in shared memory: with
             // it in registers the compiler spilled, to local memory that does
             // not stay in the 28 KB of L1 left beside the rings.
-            const uint32_t slot = bars + kSlotItem + 16 * warp;
-            if (lane == 0) st_shared_v4(slot, make_uint4(w.id, w.total, w.it.row, nq_t | w.h << 16));
+            const uint32_t slot = bars + kSlotItem + 32 * warp;
+            if (lane == 0) {
+                st_shared_v4(slot, make_uint4(w.turn, w.total, w.it.row, nq_t | w.h << 16));
+                if (PARTS) st_shared_u32(slot + 16, w.part);
+            }
             __syncwarp();
             float m = -INFINITY, l = 0.f;
             for (int c = 0; c < nc; ++c) {
@@ -707,7 +822,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int i = 0; i < kChunk / 2; ++i) sv[i] = i <= last ? sv[i] : -INFINITY;
                 }
                 if (c >= c_lo0 && c <= c_lo1) {
-                    const int h0 = a.sinks - c * kChunk - 64 * half, h1 = pos_r - a.window - c * kChunk - 64 * half;
+                    const int h0 = sinks - c * kChunk - 64 * half, h1 = pos_r - a.window - c * kChunk - 64 * half;
 #pragma unroll
                     for (int i = 0; i < kChunk / 2; ++i) sv[i] = (i < h0 || i > h1) ? sv[i] : -INFINITY;
                 }
@@ -767,14 +882,20 @@ __global__ void __launch_bounds__(kThreads, 1)
             phase ^= 2u;
             tc::fence_after_sync();
             const float lt = l + __shfl_xor_sync(0xffffffffu, l, 16);
-            const float inv = lt > 0.f ? 1.f / lt : 0.f;
+            float inv = lt > 0.f ? 1.f / lt : 0.f;
+            const uint4 kept = ld_shared_v4(slot);
+            w.turn = kept.x;
+            w.total = kept.y;
+            int part = 0;
+            float weight[kMaxParts];  // of row lane & 15 in the parts
+            if constexpr (PARTS) {
+                part = ld_shared_u32(slot + 16);
+                if (part && !leave_part(a, o_addr, m, lt, part, weight, &inv)) continue;
+            }
             // Four threads a row, 32 columns of two rows at a time, so that a
             // store of the warp covers 8 rows by 64 bytes. (Rows as the softmax
             // holds them, 16 bytes of 32 places a store, kept the stores' path
             // busy for 4000 cycles an item and all loads behind them waiting.)
-            const uint4 kept = ld_shared_v4(slot);
-            w.id = kept.x;
-            w.total = kept.y;
             const int nq_end = kept.w & 0xffff;
             const int ra = (row & ~15) + (lane >> 2), qa0 = ra >> a.lg, qa1 = (ra + 8) >> a.lg;
             const float inv0 = __shfl_sync(0xffffffffu, inv, lane >> 2);
@@ -785,8 +906,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int piece = 0; piece < 4; ++piece) {
                 float o[16];
-                tc::ld16x256_4(o_addr + 32 * piece, o);
-                tc::wait_ld();
+                if (PARTS && part) {
+                    merge_parts(a, part, piece, weight, o);
+                } else {
+                    tc::ld16x256_4(o_addr + 32 * piece, o);
+                    tc::wait_ld();
+                }
                 if (a.out_bf16) {
                     uint32_t w0[4], w1[4];
 #pragma unroll
@@ -828,8 +953,38 @@ int64_t items_bound(int B, int Hq, int Hkv, int64_t num_q) {
 
 }  // namespace
 
-size_t prefill_window_bytes(int B, int Hq, int Hkv, int num_q) {
-    return 256 + static_cast<size_t>(items_bound(B, Hq, Hkv, num_q)) * sizeof(Item);
+namespace {
+
+// Whether a call runs the kernel that cuts its last turn's items (PARTS): few
+// turns of long items, the last one filling at most half of the blocks (the
+// number of items is a guess where the sequences' query counts differ; any other
+// number is only slower). Leaving and merging the parts costs about 5 us, and the
+// code beside the softmax 1 to 4 % of all turns. Measured, us, uncut and cut: 160
+// items, W = 3300 94 and 77, W = 8192 202 and 146; 320 items 138 and 122; 624
+// items 224 and 212; 768 items, five turns and 8, 266 and 269; W = 2048: 160
+// items 64 and 62, 512 items 111 and 119. A last turn of more than half of the
+// blocks is not cut: 448 items, W = 8192, 313 and 325.
+bool cut_items(int Hq, int Hkv, int num_q, int vis_len, int num_sms) {
+    const int rows = 2 * (kRows / (Hq / Hkv));
+    const int64_t items = (static_cast<int64_t>(num_q) + rows - 1) / rows * Hkv;
+    const int64_t left = items % num_sms;
+    return vis_len >= 24 * kChunk && items < 5 * static_cast<int64_t>(num_sms) && left > 0 && 2 * left <= num_sms;
+}
+
+// The workspace: the item count (256 bytes), the items, and where items are cut
+// the arrival counts and the partial results.
+size_t item_bytes(int B, int Hq, int Hkv, int num_q) {
+    return 256 + (static_cast<size_t>(items_bound(B, Hq, Hkv, num_q)) * sizeof(Item) + 255) / 256 * 256;
+}
+
+size_t arrived_bytes(int num_sms) { return (static_cast<size_t>(num_sms) * kWarpsPerItem * 4 + 255) / 256 * 256; }
+
+}  // namespace
+
+size_t prefill_window_bytes(int B, int Hq, int Hkv, int num_q, int vis_len, int num_sms) {
+    const size_t n = item_bytes(B, Hq, Hkv, num_q);
+    if (!cut_items(Hq, Hkv, num_q, vis_len, num_sms)) return n;
+    return n + arrived_bytes(num_sms) + num_sms * kPartFloats * 4;
 }
 
 cudaError_t launch_prefill_window(const CUtensorMap& kmap, const CUtensorMap& vmap, const void* q,
@@ -837,13 +992,20 @@ cudaError_t launch_prefill_window(const CUtensorMap& kmap, const CUtensorMap& vm
                                   const int32_t* seq_lens, void* out, int* err, int B, int Hq, int Hkv,
                                   int max_blocks, int num_blocks, int max_seq_len, int max_q,
                                   float scale_log2, int window, int sinks, int out_bf16, int block_size,
-                                  int num_sms, void* ws, cudaStream_t stream) {
+                                  int vis_len, int num_sms, void* ws, cudaStream_t stream) {
     Args a{};
     a.q_start = q_start;
     a.tables = tables;
     a.seq_lens = seq_lens;
     a.num_items = static_cast<int*>(ws);
     a.items = reinterpret_cast<Item*>(static_cast<char*>(ws) + 256);
+    const bool cut = cut_items(Hq, Hkv, num_q, vis_len, num_sms);
+    if (cut) {
+        char* at = static_cast<char*>(ws) + item_bytes(B, Hq, Hkv, num_q);
+        a.arrived = reinterpret_cast<int*>(at);
+        a.parts = reinterpret_cast<float*>(at + arrived_bytes(num_sms));
+    }
+    a.num_sms = num_sms;
     a.out = out;
     a.err = err;
     a.B = B;
@@ -883,11 +1045,13 @@ cudaError_t launch_prefill_window(const CUtensorMap& kmap, const CUtensorMap& vm
     if (e != cudaSuccess) return e;
     e = cudaLaunchKernelEx(&cfg, items, a);
     if (e != cudaSuccess) return e;
-    auto kern = block_size == 16 ? window_kernel<16> : window_kernel<32>;
+    auto kern = cut ? (block_size == 16 ? window_kernel<16, true> : window_kernel<32, true>)
+                    : (block_size == 16 ? window_kernel<16, false> : window_kernel<32, false>);
     e = cudaFuncSetAttribute(reinterpret_cast<const void*>(kern), cudaFuncAttributeMaxDynamicSharedMemorySize,
                              static_cast<int>(kSmemBytes));
     if (e != cudaSuccess) return e;
-    cfg.gridDim = dim3(static_cast<unsigned>(std::min<int64_t>(num_sms, static_cast<int64_t>(a.max_items) * Hkv)));
+    cfg.gridDim = dim3(static_cast<unsigned>(
+        cut ? num_sms : std::min<int64_t>(num_sms, static_cast<int64_t>(a.max_items) * Hkv)));
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = kSmemBytes;
     return cudaLaunchKernelEx(&cfg, kern, kmap, vmap, qmap, a);

@@ -271,6 +271,46 @@ def test_prefill_sizes(lens, ns, W, S):
     assert bool(torch.isfinite(out).all())
 
 
+@pytest.mark.parametrize("Hq,Hkv,lens,ns,W,S", [
+    (8, 2, [5000], [64], 4096, 5),                    # four parts of nine chunks and less
+    (8, 2, [6000], [40], 4090, 64),
+    (8, 2, [4500, 1500, 30], [40, 64, 17], 4096, 600),  # parts, two of eight chunks and four, and none
+    (4, 4, [6000, 400], [256, 100], 4000, 0),         # rows that see nothing of the last part
+    (8, 1, [9000], [128], 6000, 2000),
+    (8, 2, [4300] * 80, [50] * 80, 4096, 4),          # a complete turn of the blocks before
+])
+@pytest.mark.parametrize("bs", [16, 32])
+def test_prefill_items_in_parts(Hq, Hkv, lens, ns, W, S, bs):
+    c = Case(lens, ns, Hq=Hq, Hkv=Hkv, W=W, S=S, bs=bs, seed=W).upload()
+    pa.pa_debug_set_prefill_kernel(pa.PA_PREFILL_TWO_TILE)
+    try:
+        out = c.run(prefill=True)
+        again = [c.run(prefill=True) for _ in range(3)]
+        f32 = c.run(prefill=True, out_dtype=torch.float32)
+    finally:
+        pa.pa_debug_set_prefill_kernel(pa.PA_PREFILL_AUTO)
+    rows = set(range(0, c.T, 1 + c.T // 60)) | {c.T - 1}
+    c.check(out, prefill=True, rows=rows)
+    c.check(f32, prefill=True, rows=rows)
+    assert bool(torch.isfinite(out).all())
+    for x in again:                  # the parts are merged in one order
+        assert torch.equal(out, x)
+
+
+def test_prefill_parts_show_nan_of_a_visible_key():
+    c = Case([5000], [40], W=4500, S=4, seed=3)
+    last = 4999                      # only the last query sees it, in the last part
+    c.k[int(c.table[0, last // c.bs]), :, last % c.bs] = float("nan")
+    c.upload()
+    pa.pa_debug_set_prefill_kernel(pa.PA_PREFILL_TWO_TILE)
+    try:
+        out = c.run(prefill=True)
+    finally:
+        pa.pa_debug_set_prefill_kernel(pa.PA_PREFILL_AUTO)
+    assert bool(torch.isnan(out[-1]).all())
+    c.check(out, prefill=True, rows=set(range(39)))
+
+
 def test_prefill_of_single_queries_is_the_decode():
     c = Case([1, 40, 300, 1000], W=64, S=4).upload()
     c.check(c.run(prefill=True), prefill=True)
