@@ -485,7 +485,7 @@ def _refuse(what: str, dev: int, args) -> None:
     raise ValueError(f"{what}: unsupported tensors")
 
 
-def _stream(dev: int, stream) -> int:
+def _stream_of(dev: int, stream) -> int:
     """A stream's handle: by default device ``dev``'s current stream."""
     if stream is None:
         return torch._C._cuda_getCurrentRawStream(dev)
@@ -561,7 +561,7 @@ def pa_step_maps(cache_lens: torch.Tensor, new_lens: torch.Tensor, free_blocks: 
         cache_lens.data_ptr(), new_lens.data_ptr(), B,
         free_blocks.data_ptr() or count, F, count, block_tables.data_ptr(), MB, int(block_size),
         int(num_blocks), min(int(max_seq_len), _INT_MAX), seq_lens.data_ptr(), q_start.data_ptr(),
-        positions.data_ptr(), slots.data_ptr(), T, free_left.data_ptr(), err, _stream(dev, stream)))
+        positions.data_ptr(), slots.data_ptr(), T, free_left.data_ptr(), err, _stream_of(dev, stream)))
 
 
 def pa_qk_rope(q: torch.Tensor, k: torch.Tensor, positions: torch.Tensor, rope: Rope | None,
@@ -594,7 +594,7 @@ def pa_qk_rope(q: torch.Tensor, k: torch.Tensor, positions: torch.Tensor, rope: 
         None if q_weight is None else q_weight.data_ptr(),
         None if k_weight is None else k_weight.data_ptr(), float(eps),
         None if rope is None else rope.address, q_out.data_ptr(), _rows(what, "q_out", q_out, T, Hq, D),
-        k_out.data_ptr(), _rows(what, "k_out", k_out, T, Hk, D), _stream(dev, stream)))
+        k_out.data_ptr(), _rows(what, "k_out", k_out, T, Hk, D), _stream_of(dev, stream)))
 
 
 def pa_qk_rope_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, positions: torch.Tensor,
@@ -636,7 +636,7 @@ def pa_qk_rope_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, positio
         None if q_weight is None else q_weight.data_ptr(),
         None if k_weight is None else k_weight.data_ptr(), float(eps),
         None if rope is None else rope.address, q_out.data_ptr(), _rows(what, "q_out", q_out, T, Hq, D),
-        k_pool.data_ptr(), v_pool.data_ptr(), bs, NB, err, _stream(dev, stream)))
+        k_pool.data_ptr(), v_pool.data_ptr(), bs, NB, err, _stream_of(dev, stream)))
 
 
 def _check_window(what: str, q, k_pool, v_pool, block_tables, seq_lens, out, B: int) -> tuple:
@@ -674,7 +674,7 @@ def pa_decode_window(q: torch.Tensor, k_pool: torch.Tensor, v_pool: torch.Tensor
         k_pool.data_ptr(), v_pool.data_ptr(), block_tables.data_ptr(), MB, seq_lens.data_ptr(), B,
         Hq, Hkv, D, bs, NB, min(int(max_seq_len), _INT_MAX), float(scale), min(int(window), _INT_MAX),
         min(int(sinks), _INT_MAX), _dtype(q), out.data_ptr(),
-        _dtype(out), ctypes.byref(plan.handle), _stream(dev, stream)))
+        _dtype(out), ctypes.byref(plan.handle), _stream_of(dev, stream)))
     return out
 
 
@@ -699,7 +699,7 @@ def pa_prefill_window(q: torch.Tensor, q_start: torch.Tensor, k_pool: torch.Tens
         k_pool.data_ptr(), v_pool.data_ptr(), block_tables.data_ptr(), MB, seq_lens.data_ptr(), B,
         Hq, Hkv, D, bs, NB, min(int(max_seq_len), _INT_MAX), float(scale), min(int(window), _INT_MAX),
         min(int(sinks), _INT_MAX), _dtype(q), out.data_ptr(),
-        _dtype(out), ctypes.byref(plan.handle), _stream(dev, stream)))
+        _dtype(out), ctypes.byref(plan.handle), _stream_of(dev, stream)))
     return out
 
 
