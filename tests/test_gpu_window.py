@@ -426,6 +426,54 @@ def test_expired_waits_are_reported_and_the_next_call_is_right(prefill):
     c.check(c.run(prefill=prefill), prefill)
 
 
+# The persistent kernel, whole items and items in parts.
+PERSISTENT = [dict(lens=[700, 90], ns=[70, 20], W=200, S=4), dict(lens=[5000], ns=[40], W=4500, S=4)]
+
+
+@pytest.mark.parametrize("kw", PERSISTENT)
+def test_expired_waits_of_the_persistent_kernel(kw):
+    c = Case(**kw).upload()
+    pa.pa_debug_set_prefill_kernel(pa.PA_PREFILL_TWO_TILE)
+    try:
+        c.run(prefill=True)
+        torch.cuda.synchronize()
+        pa.pa_debug_set_wait_probe(True)
+        try:
+            c.run(prefill=True)
+            assert pa.pa_last_device_error(c.plan) == pa.PA_DEVERR_TIMEOUT
+        finally:
+            pa.pa_debug_set_wait_probe(False)
+        for _ in range(2):
+            c.check(c.run(prefill=True), prefill=True)
+    finally:
+        pa.pa_debug_set_prefill_kernel(pa.PA_PREFILL_AUTO)
+
+
+@pytest.mark.parametrize("kw", PERSISTENT)
+def test_graph_of_the_persistent_kernel(kw):
+    c = Case(seed=1, **kw).upload()
+    out = torch.zeros(c.q.shape, dtype=torch.bfloat16, device="cuda")
+    pa.pa_debug_set_prefill_kernel(pa.PA_PREFILL_TWO_TILE)
+    try:
+        c.run(prefill=True, out=out)
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            c.run(prefill=True, out=out)
+    finally:
+        pa.pa_debug_set_prefill_kernel(pa.PA_PREFILL_AUTO)
+    for seed in (2, 3):
+        other = Case(seed=seed, **kw)
+        for name in ("q", "k", "v"):
+            c.d[name].copy_(getattr(other, name))
+        c.d["table"].copy_(torch.from_numpy(other.table))
+        out.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        other.plan = c.plan
+        other.check(out, prefill=True)
+
+
 def test_binding_refuses_shapes_and_types():
     c = Case([70, 9], W=30, S=2).upload()
     for name, t, e in (("lens", c.d["lens"][:1], ValueError), ("lens", c.d["lens"].long(), TypeError),
