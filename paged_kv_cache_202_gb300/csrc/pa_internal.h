@@ -150,6 +150,8 @@ cudaError_t launch_split_window(const SplitLaunch& L, const CUtensorMap& kmap,
 // Host-side planning of a split launch, shared by pa_decode,
 // pa_decode_multi and pa_decode_noalloc.
 constexpr size_t kSmemLimit = 232448;  // opt-in dynamic shared memory per block on sm_10x
+// The same for the kernels that call split::scan_lengths, whose static array counts too.
+constexpr size_t kScanSmemLimit = kSmemLimit - 32 * sizeof(int);
 constexpr int kMaxBatch = 8192;        // per-sequence arrays live in shared memory
 constexpr int64_t kMaxRows = int64_t(1) << 30;  // output rows (rows x heads), counted in int
 constexpr int kSms = 152;              // of the GB300, for grids that need no plan

@@ -88,9 +88,11 @@ int split_blocks_per_sm(const SplitLaunch& L, cudaError_t* status) {
         *status = cudaErrorInvalidValue;
         return 0;
     }
+    // The limit belongs to the function in the whole process, whose other calls
+    // have other sizes: the most that any of them takes.
     cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void*>(fn),
                                          cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         static_cast<int>(L.smem));
+                                         static_cast<int>(kScanSmemLimit));
     if (e != cudaSuccess) {
         *status = e;
         return 0;

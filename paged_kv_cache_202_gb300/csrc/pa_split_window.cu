@@ -38,9 +38,10 @@ WindowFn select_window(const SplitLaunch& L) {
 int split_window_blocks_per_sm(const SplitLaunch& L, cudaError_t* status) {
     split::WindowFn fn = split::select_window(L);
     int n = 0;
+    // For every call in the process, whatever its size (as in pa_split.cu).
     *status = fn ? cudaFuncSetAttribute(reinterpret_cast<const void*>(fn),
                                         cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                        static_cast<int>(L.smem))
+                                        static_cast<int>(kScanSmemLimit))
                  : cudaErrorInvalidValue;
     if (*status == cudaSuccess)
         *status = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, reinterpret_cast<const void*>(fn),
