@@ -172,8 +172,8 @@ bool split_shape(int kind, int nq, int B, int Hq, int Hkv, int D, int block_size
         s.q_bytes = round_up(static_cast<size_t>(s.GS) * mq_q_pitch(D), 16);
         const size_t per_warp = s.stage_bytes + s.q_bytes + 8 + 16;  // ring, rows, barrier, record
         const size_t fixed = 1024 + s.lens_bytes + 16 + 16;         // alignment, arrays, padding, probe
-        if (fixed >= kSmemLimit) return false;
-        s.warps = static_cast<int>(std::min<size_t>(kQsMaxWarps, (kSmemLimit - fixed) / per_warp));
+        if (fixed >= kScanSmemLimit) return false;
+        s.warps = static_cast<int>(std::min<size_t>(kQsMaxWarps, (kScanSmemLimit - fixed) / per_warp));
         if (s.warps < 1) return false;
     } else {
         // K and V of a chunk, then the segment's query rows (read once per
@@ -189,7 +189,7 @@ bool split_shape(int kind, int nq, int B, int Hq, int Hkv, int D, int block_size
              round_up(static_cast<size_t>(s.warps) * s.stages * 8, 16) +
              static_cast<size_t>(s.warps) * s.stages * 16 + 16 +
              static_cast<size_t>(s.warps) * s.q_bytes;
-    if (s.smem > kSmemLimit) return false;
+    if (s.smem > kScanSmemLimit) return false;
     *out = s;
     return true;
 }

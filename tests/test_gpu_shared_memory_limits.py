@@ -67,3 +67,13 @@ def test_split_windowed_decodes_of_different_sizes(groups, one_plan):
         c = cases[Hq]
         c.check(c.run())
         assert c.plan.info()[1] > 8      # the split kernels, not a cluster
+
+
+@pytest.mark.parametrize("B,Hq", [(512, 9), (600, 9), (6783, 36)])
+@pytest.mark.parametrize("noalloc", [False, True])
+def test_decodes_that_fill_the_shared_memory(B, Hq, noalloc):
+    # Sizes at which the stages, the query rows and the lengths come within a
+    # few bytes of what a block may have.
+    c = small(B, Hq)
+    with pa.Plan() as plan:
+        c.compare(plain(c, plan, noalloc), rows=set(range(0, B, B // 8)))
