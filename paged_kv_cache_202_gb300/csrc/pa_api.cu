@@ -89,34 +89,45 @@ namespace pa {
 int wait_probe() { return g_wait_probe.load(std::memory_order_relaxed); }
 int prefill_kernel_choice() { return g_prefill_kernel.load(std::memory_order_relaxed); }
 
-bool encode_pool_map(CUtensorMap* map, const void* pool, int rows, int D, int BS) {
+namespace {
+
+// A tensor map of a 3-D bf16 array with the 128-byte swizzle. The driver's call
+// wants a context on the calling thread, which the runtime's earlier calls need
+// not have bound on a thread of the caller's that is new to CUDA: a failed call
+// binds the current device's and tries once more.
+bool encode_map(CUtensorMap* map, const void* base, const cuuint64_t (&dims)[3], const cuuint64_t (&strides)[2],
+                const cuuint32_t (&box)[3]) {
     auto fn = encode_fn();
     if (!fn) return false;
-    cuuint64_t dims[3] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(BS),
-                          static_cast<cuuint64_t>(rows)};
-    cuuint64_t strides[2] = {static_cast<cuuint64_t>(D) * 2, static_cast<cuuint64_t>(BS) * D * 2};
-    cuuint32_t box[3] = {64, static_cast<cuuint32_t>(BS), 1};
-    cuuint32_t estr[3] = {1, 1, 1};
-    CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(pool), dims, strides,
-                    box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-    return r == CUDA_SUCCESS;
+    const cuuint32_t estr[3] = {1, 1, 1};
+    auto encode = [&] {
+        return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    };
+    if (encode()) return true;
+    int dev = 0;
+    return cudaGetDevice(&dev) == cudaSuccess && cudaSetDevice(dev) == cudaSuccess && encode();
+}
+
+}  // namespace
+
+bool encode_pool_map(CUtensorMap* map, const void* pool, int rows, int D, int BS) {
+    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(BS),
+                                static_cast<cuuint64_t>(rows)};
+    const cuuint64_t strides[2] = {static_cast<cuuint64_t>(D) * 2, static_cast<cuuint64_t>(BS) * D * 2};
+    const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(BS), 1};
+    return encode_map(map, pool, dims, strides, box);
 }
 
 bool encode_query_map(CUtensorMap* map, const void* q, int T, int Hq, int g, int Qb) {
     // q [T][Hq][D = 128] bf16 as (D, Hq, T); one box = one 64-column half of a
     // query tile: Qb queries x the g heads of a kv head, rows in (query, head)
     // order, 128-byte swizzle (the K-major layout of the tile's MMA operand).
-    auto fn = encode_fn();
-    if (!fn) return false;
-    cuuint64_t dims[3] = {128, static_cast<cuuint64_t>(Hq), static_cast<cuuint64_t>(T)};
-    cuuint64_t strides[2] = {128 * 2, static_cast<cuuint64_t>(Hq) * 128 * 2};
-    cuuint32_t box[3] = {64, static_cast<cuuint32_t>(g), static_cast<cuuint32_t>(Qb)};
-    cuuint32_t estr[3] = {1, 1, 1};
-    CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(q), dims, strides,
-                    box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-    return r == CUDA_SUCCESS;
+    const cuuint64_t dims[3] = {128, static_cast<cuuint64_t>(Hq), static_cast<cuuint64_t>(T)};
+    const cuuint64_t strides[2] = {128 * 2, static_cast<cuuint64_t>(Hq) * 128 * 2};
+    const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(g), static_cast<cuuint32_t>(Qb)};
+    return encode_map(map, q, dims, strides, box);
 }
 
 bool split_shape(int kind, int nq, int B, int Hq, int Hkv, int D, int block_size, int max_blocks,
