@@ -1039,9 +1039,11 @@ cudaError_t launch_prefill_window(const CUtensorMap& kmap, const CUtensorMap& vm
     cfg.blockDim = dim3(kItemThreads);
     cfg.dynamicSmemBytes = (2 * static_cast<size_t>(B) + 1) * sizeof(int);
     auto items = block_size == 16 ? window_items_kernel<16> : window_items_kernel<32>;
+    // The limit belongs to the function, which other threads launch with other
+    // batches: that of the largest.
     cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void*>(items),
                                          cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         static_cast<int>(cfg.dynamicSmemBytes));
+                                         static_cast<int>((2 * kMaxBatch + 1) * sizeof(int)));
     if (e != cudaSuccess) return e;
     e = cudaLaunchKernelEx(&cfg, items, a);
     if (e != cudaSuccess) return e;

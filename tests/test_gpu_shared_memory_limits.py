@@ -3,6 +3,9 @@ after the other and at the same time. The limit on a kernel's dynamic shared
 memory belongs to the function in the whole process, so what one call sets
 must do for every other call, whatever its plan, thread or sizes."""
 
+import ctypes
+import subprocess
+
 import numpy as np
 import pytest
 import torch
@@ -77,3 +80,81 @@ def test_decodes_that_fill_the_shared_memory(B, Hq, noalloc):
     c = small(B, Hq)
     with pa.Plan() as plan:
         c.compare(plain(c, plan, noalloc), rows=set(range(0, B, B // 8)))
+
+
+# Two threads in C, which meet more often than Python's: each makes one call
+# again and again, its arguments as 64-bit words (the scale in millionths).
+HAMMER = r"""
+#include <pthread.h>
+typedef long long w;
+typedef void* p;
+typedef int (*prefill)(p, p, int, int, p, p, p, int, p, int, int, int, int, int, int, int, float, int, int, int, p, int, p, p);
+typedef int (*maps)(p, p, int, p, int, p, p, int, int, int, int, p, p, p, p, int, p, p, p);
+typedef int (*scores)(p, p, p, int, p, int, int, int, int, int, int, int, p, p, p, p);
+struct job { int kind; p f; const w* a; int times, status; };
+#define P(i) ((p)a[i])
+#define I(i) ((int)a[i])
+static int call(int kind, p f, const w* a) {
+    if (kind == 0)
+        return ((prefill)f)(P(0), P(1), I(2), I(3), P(4), P(5), P(6), I(7), P(8), I(9), I(10), I(11), I(12), I(13), I(14),
+                            I(15), a[16] * 1e-6f, I(17), I(18), I(19), P(20), I(21), P(22), P(23));
+    if (kind == 1)
+        return ((maps)f)(P(0), P(1), I(2), P(3), I(4), P(5), P(6), I(7), I(8), I(9), I(10), P(11), P(12), P(13), P(14),
+                         I(15), P(16), P(17), P(18));
+    return ((scores)f)(P(0), P(1), P(2), I(3), P(4), I(5), I(6), I(7), I(8), I(9), I(10), I(11), P(12), P(13), P(14), P(15));
+}
+static void* work(void* x) {
+    struct job* j = x;
+    for (int i = 0; i < j->times && j->status == 0; ++i) j->status = call(j->kind, j->f, j->a);
+    return 0;
+}
+int hammer(int kind, p f, const w* a, const w* b, int times) {
+    struct job j[2] = {{kind, f, a, times, 0}, {kind, f, b, times, 0}};
+    pthread_t t[2];
+    for (int i = 0; i < 2; ++i) pthread_create(&t[i], 0, work, &j[i]);
+    for (int i = 0; i < 2; ++i) pthread_join(t[i], 0);
+    return j[0].status ? j[0].status : j[1].status;
+}
+"""
+PREFILL, MAPS, SCORES = range(3)
+
+
+@pytest.fixture(scope="module")
+def hammer(tmp_path_factory):
+    at = tmp_path_factory.mktemp("hammer")
+    (at / "hammer.c").write_text(HAMMER)
+    subprocess.run(["gcc", "-O1", "-shared", "-fPIC", "-pthread", "-o", at / "hammer.so", at / "hammer.c"], check=True)
+    f = ctypes.CDLL(str(at / "hammer.so")).hammer
+    f.argtypes = [ctypes.c_int, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int]
+
+    def run(kind, fn, first, second, times):
+        streams = [torch.cuda.Stream() for _ in range(2)]   # the last argument of every call
+        words = [(ctypes.c_longlong * (len(a) + 1))(*[x or 0 for x in a], s.cuda_stream)
+                 for a, s in zip((first, second), streams)]
+        torch.cuda.synchronize()
+        assert f(kind, ctypes.cast(fn, ctypes.c_void_p), *words, times) == pa.PA_OK
+        torch.cuda.synchronize()
+    return run
+
+
+def test_windowed_prefills_of_two_threads(hammer):
+    rng = np.random.default_rng(1)
+    cases = [Case(rng.integers(1, 40, size=B).tolist(), [1] * B, Hq=2, Hkv=1, W=16, S=0, seed=B, scale=0.125).upload()
+             for B in (7000, 3)]
+    p = lambda t: t.data_ptr()  # noqa: E731
+    pa.pa_debug_set_prefill_kernel(pa.PA_PREFILL_TWO_TILE)
+    try:
+        want = [c.run(prefill=True) for c in cases]
+        got = [torch.zeros_like(w) for w in want]
+        args = []
+        for c, out in zip(cases, got):
+            d = c.d
+            args.append((p(d["q"]), p(d["start"]), c.T, 1, p(d["k"]), p(d["v"]), p(d["table"]), c.MB, p(d["lens"]), c.B,
+                         2, 1, 128, c.bs, c.NB, max(c.lens), 125000, c.W, c.S, pa.PA_BF16, p(out), pa.PA_BF16,
+                         ctypes.addressof(c.plan.handle)))
+        hammer(PREFILL, pa.lib().pa_prefill_window, *args, times=3000)
+    finally:
+        pa.pa_debug_set_prefill_kernel(pa.PA_PREFILL_AUTO)
+    for c, w, g in zip(cases, want, got):
+        assert torch.equal(w, g)
+        c.check(g, prefill=True, rows=set(range(0, c.B, max(1, c.B // 40))))
