@@ -235,10 +235,12 @@ extern "C" pa_status pa_step_maps(const int32_t* cache_lens, const int32_t* new_
     cfg.blockDim = dim3(pa::kStepThreads);
     cfg.dynamicSmemBytes = (2 * static_cast<size_t>(B) + 1) * 4;
     cfg.stream = reinterpret_cast<cudaStream_t>(stream);
+    // Above the default limit, that of the largest batch: it belongs to the
+    // function, which other threads launch with other batches.
     if (cfg.dynamicSmemBytes > 46 * 1024 &&
         cudaFuncSetAttribute(reinterpret_cast<const void*>(pa::step_maps_kernel),
                              cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             static_cast<int>(cfg.dynamicSmemBytes)) != cudaSuccess)
+                             (2 * pa::kMaxBatch + 1) * 4) != cudaSuccess)
         return PA_ERR_CUDA;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

@@ -158,3 +158,20 @@ def test_windowed_prefills_of_two_threads(hammer):
     for c, w, g in zip(cases, want, got):
         assert torch.equal(w, g)
         c.check(g, prefill=True, rows=set(range(0, c.B, max(1, c.B // 40))))
+
+
+def test_step_maps_of_two_threads(hammer):
+    from test_gpu_step_maps import Step, check
+    p = lambda t: t.data_ptr()  # noqa: E731
+    steps = [Step([5] * B, [1] * B).upload() for B in (8192, 6000)]
+    args = []
+    for s in steps:
+        s.call()
+        check(s)
+        d, o = s.d, s.o
+        args.append((p(d["cache"]), p(d["new"]), s.B, p(d["free"]), len(s.free), p(d["count"]), p(d["table"]),
+                     s.MB, s.bs, s.NB, s.limit, p(o["seq"]), p(o["start"]), p(o["pos"]), p(o["slots"]), s.T,
+                     p(o["left"]), p(o["err"])))
+    hammer(MAPS, pa.lib().pa_step_maps, *args, times=10000)
+    for s in steps:
+        check(s)
