@@ -314,9 +314,11 @@ cudaError_t launch_scores(ScoreArgs a, bool bf16, int num_sms, cudaStream_t stre
                         static_cast<size_t>(kScoreWarps) * a.stages * (8 + 4) + 8;
     a.probe_wait = wait_probe();
     auto kern = bf16 ? page_score_kernel<BS, uint16_t> : page_score_kernel<BS, float>;
+    // The limit belongs to the function, which other threads launch with other
+    // sizes: the most that any of them takes.
     cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void*>(kern),
                                          cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         static_cast<int>(smem));
+                                         static_cast<int>(kScanSmemLimit));
     if (e != cudaSuccess) return e;
     int per_sm = 0;
     e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, reinterpret_cast<const void*>(kern),

@@ -175,3 +175,25 @@ def test_step_maps_of_two_threads(hammer):
     hammer(MAPS, pa.lib().pa_step_maps, *args, times=10000)
     for s in steps:
         check(s)
+
+
+def test_page_scores_of_two_threads(hammer):
+    def inputs(B, Hkv, D, NB=50, bs=16):
+        g = torch.Generator(device="cuda")
+        g.manual_seed(B)
+        k, v = (torch.randn(NB, Hkv, bs, D, generator=g, device="cuda").bfloat16() for _ in range(2))
+        table = torch.randint(0, NB, (B, 4), generator=g, device="cuda", dtype=torch.int32)
+        lens = torch.randint(1, 64, (B,), generator=g, device="cuda", dtype=torch.int32)
+        return [k, v, table, lens, torch.zeros(B, 4, device="cuda"), torch.zeros(B, dtype=torch.int32, device="cuda")]
+
+    p = lambda t: t.data_ptr()  # noqa: E731
+    data, args, want = [inputs(2000, 1, 128), inputs(3, 1, 64)], [], []
+    for k, v, table, lens, scores, victims in data:
+        pa.pa_page_scores(k, v, table, lens, 64, scores, victims)
+        torch.cuda.synchronize()
+        want.append((scores.clone(), victims.clone()))
+        args.append((p(k), p(v), p(table), 4, p(lens), len(lens), 1, k.shape[3], 16, 50, 64, pa.PA_BF16,
+                     p(scores), p(victims), None))
+    hammer(SCORES, pa.lib().pa_page_scores, *args, times=5000)
+    for w, (*_, scores, victims) in zip(want, data):
+        assert torch.equal(w[0], scores) and torch.equal(w[1], victims)
