@@ -84,22 +84,22 @@ __device__ __forceinline__ float sumsq16<float>(const uint4 w) {
 // token so that the eight rows a quarter-warp reads hit different banks; after
 // the last head of a page the halves are joined, the token ratios formed and
 // averaged, and lane 0 writes the page score.
-constexpr int kScoreWarps = 8;
+constexpr int kScoreWarps = 8;  // at most, fewer where their stages do not fit
 
 template <int BS, typename T>
 __global__ void __launch_bounds__(kScoreWarps * 32, 1) page_score_kernel(const ScoreArgs a) {
     constexpr int TPL = BS / 16;  // tokens per lane
     extern __shared__ uint8_t smem_raw[];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, W = blockDim.x >> 5;
     const uint32_t raw = smem_addr(smem_raw);
     const uint32_t base = (raw + 127u) & ~127u;
     int* pre = reinterpret_cast<int*>(smem_raw + (base - raw));
     int* len = pre + (a.B + 1);
     const uint32_t ring0 = base + a.lens_bytes;
-    const uint32_t bars0 = ring0 + kScoreWarps * a.stages * a.stage_bytes;
+    const uint32_t bars0 = ring0 + W * a.stages * a.stage_bytes;
     // After the barriers and page records: an mbarrier that nothing completes
     // (the wait-expiry probe's first wait).
-    const uint32_t probe_bar = bars0 + kScoreWarps * a.stages * 12;
+    const uint32_t probe_bar = bars0 + (W * a.stages * 12 + 7 & ~7);
     if (threadIdx.x == 0 && a.probe_wait) {
         mbar_init(probe_bar, 1);
         fence_barrier_init();
@@ -108,7 +108,7 @@ __global__ void __launch_bounds__(kScoreWarps * 32, 1) page_score_kernel(const S
     split::scan_lengths<BS>(a.seq_lens, a.B, limit, pre, len, a.err);
 
     const int P = pre[a.B];
-    const int NW = gridDim.x * kScoreWarps;
+    const int NW = gridDim.x * W;
     // Static ranges over the first part of the page list, then pieces of qd
     // pages (none for small lists, whose static ranges are already short).
     const int qd = kScoreDynPages;
@@ -117,10 +117,10 @@ __global__ void __launch_bounds__(kScoreWarps * 32, 1) page_score_kernel(const S
                        : 0;
     const int A = P - Dp, nd = Dp / qd;
     const int per = (A + NW - 1) / NW;
-    const int gw = blockIdx.x * kScoreWarps + warp;
+    const int gw = blockIdx.x * W + warp;
     const int S = a.stages, H = a.Hkv;
     const uint32_t my_bars = bars0 + warp * S * 8;
-    const uint32_t my_xs = bars0 + kScoreWarps * S * 8 + warp * S * 4;  // page of each stage
+    const uint32_t my_xs = bars0 + W * S * 8 + warp * S * 4;  // page of each stage
     const uint32_t my_ring = ring0 + warp * S * a.stage_bytes;
 
     // Issue range [ix, ix1): the warp's static range, then claimed pieces.
@@ -309,9 +309,14 @@ cudaError_t launch_scores(ScoreArgs a, bool bf16, int num_sms, cudaStream_t stre
     const int esize = bf16 ? 2 : 4;
     a.stage_bytes = 2 * BS * a.D * esize;               // K and V page of one (block, head)
     a.lens_bytes = static_cast<int>((static_cast<size_t>(2 * a.B + 1) * 4 + 127) / 128 * 128);
-    a.stages = std::max(1, std::min(8, (192 * 1024) / (kScoreWarps * a.stage_bytes)));
-    const size_t smem = 128 + a.lens_bytes + static_cast<size_t>(kScoreWarps) * a.stages * a.stage_bytes +
-                        static_cast<size_t>(kScoreWarps) * a.stages * (8 + 4) + 8;
+    // 192 KB of stages, or what the lengths of many sequences leave: as many as
+    // every warp can have, and fewer warps where one each is too much.
+    const size_t fixed = 128 + a.lens_bytes + 16;
+    const size_t room = std::min<size_t>(192 * 1024 + kScoreWarps * 8 * (8 + 4), kScanSmemLimit - fixed);
+    const size_t per_stage = a.stage_bytes + 8 + 4;
+    const int warps = static_cast<int>(std::min<size_t>(kScoreWarps, room / per_stage));
+    a.stages = static_cast<int>(std::min<size_t>(8, room / (warps * per_stage)));
+    const size_t smem = fixed + static_cast<size_t>(warps) * a.stages * per_stage;
     a.probe_wait = wait_probe();
     auto kern = bf16 ? page_score_kernel<BS, uint16_t> : page_score_kernel<BS, float>;
     // The limit belongs to the function, which other threads launch with other
@@ -322,18 +327,18 @@ cudaError_t launch_scores(ScoreArgs a, bool bf16, int num_sms, cudaStream_t stre
     if (e != cudaSuccess) return e;
     int per_sm = 0;
     e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, reinterpret_cast<const void*>(kern),
-                                                      kScoreWarps * 32, smem);
+                                                      warps * 32, smem);
     if (e != cudaSuccess) return e;
     const int64_t max_pages = static_cast<int64_t>(a.B) *
                               ((std::min(a.max_seq_len, a.max_blocks * BS) + BS - 1) / BS);
-    const int64_t need = (max_pages + kScoreWarps * 4 - 1) / (kScoreWarps * 4);
+    const int64_t need = (max_pages + warps * 4 - 1) / (warps * 4);
     const int blocks = static_cast<int>(std::max<int64_t>(
         1, std::min<int64_t>(need, static_cast<int64_t>(std::max(per_sm, 1)) * num_sms)));
     // victims[0] counts the claimed pieces during the score kernel; the victim
     // kernel overwrites it afterwards.
     e = cudaMemsetAsync(a.victims, 0, sizeof(int32_t), stream);
     if (e != cudaSuccess) return e;
-    kern<<<blocks, kScoreWarps * 32, smem, stream>>>(a);
+    kern<<<blocks, warps * 32, smem, stream>>>(a);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     victim_kernel<<<(a.B + 3) / 4, 128, 0, stream>>>(a, BS);

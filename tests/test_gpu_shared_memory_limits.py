@@ -197,3 +197,32 @@ def test_page_scores_of_two_threads(hammer):
     hammer(SCORES, pa.lib().pa_page_scores, *args, times=5000)
     for w, (*_, scores, victims) in zip(want, data):
         assert torch.equal(w[0], scores) and torch.equal(w[1], victims)
+
+
+@pytest.mark.parametrize("B,D,bs,dtype", [
+    (8192, 128, 16, torch.bfloat16), (8192, 64, 32, torch.float32), (4500, 128, 16, torch.bfloat16),
+    (9, 128, 32, torch.float32), (8192, 128, 32, torch.float32),
+])
+def test_page_scores_of_many_sequences_and_large_pages(B, D, bs, dtype):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(B + D)
+    k, v = (torch.randn(40, 2, bs, D, generator=g, device="cuda").to(dtype) for _ in range(2))
+    table = torch.randint(0, 40, (B, 3), generator=g, device="cuda", dtype=torch.int32)
+    lens = torch.randint(1, 3 * bs + 1, (B,), generator=g, device="cuda", dtype=torch.int32)
+    scores = torch.full((B, 3), -7.0, device="cuda")
+    victims = torch.zeros(B, dtype=torch.int32, device="cuda")
+    pa.pa_page_scores(k, v, table, lens, 3 * bs, scores, victims)
+    torch.cuda.synchronize()
+    norm = lambda x: x.double().pow(2).sum((1, 3)).sqrt()  # noqa: E731
+    ratio = (norm(v) / norm(k))[table.long()]                     # [B, 3, bs]
+    left = (lens[:, None] - torch.arange(3, device="cuda") * bs).clamp(0, bs)
+    valid = torch.arange(bs, device="cuda") < left[:, :, None]
+    want = (ratio * valid).sum(-1) / left.clamp(min=1)
+    # Sums of 2 D squares and a mean of bs quotients in 32 bits: below 1e-4 of the value.
+    assert bool(((scores - want).abs() <= 1e-4 * want)[left > 0].all())
+    assert bool((scores[left == 0] == -7.0).all())
+    full = lens % bs == 0
+    assert bool((victims[~full] == -1).all())
+    at = victims.long().clamp(min=0)
+    least = torch.where(left == bs, want, torch.inf).min(1).values
+    assert bool((want.gather(1, at[:, None])[:, 0] <= least * (1 + 2e-4))[full].all())
