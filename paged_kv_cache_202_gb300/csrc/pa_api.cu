@@ -315,7 +315,8 @@ struct pa_plan {
     int sched_permille = -1, sched_pages = 0;  // forced dynamic tail (pa_plan_set_schedule)
     int merge_mode = PA_MERGE_AUTO;             // pa_plan_set_merge
     int last_fused = 0;
-    size_t cnt_clean = 0;  // bytes at the end of the workspace known to be zero
+    int* cnt = nullptr;    // the fused merge's segment counters, zero between calls
+    size_t cnt_bytes = 0;
     int last_path = 0, last_blocks = 0, last_warps = 0;
     // After a windowed call, workspaces that a call outgrows are kept until
     // pa_free: a captured graph may still use them.
@@ -408,7 +409,38 @@ pa_status grow_workspace(pa_plan* plan, size_t need, cudaStream_t stream) {
     if (plan->ws) plan->retired.push_back(plan->ws);
     plan->ws = ws;
     plan->ws_bytes = need;
-    plan->cnt_clean = need;
+    return PA_OK;
+}
+
+// The fused merge's segment counters, `bytes` of them, in memory of their own:
+// other calls, and graphs captured with the plan, write anywhere in the
+// workspace. A fused call leaves them zero. A capture before the first eager
+// fused call, in which nothing can be allocated, takes `spare` instead (the end
+// of the workspace) and clears it in the graph.
+pa_status fused_counters(pa_plan* plan, size_t bytes, char* spare, cudaStream_t stream, int** cnt) {
+    if (plan->cnt_bytes < bytes) {
+        cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
+        if (cudaStreamIsCapturing(stream, &cap) != cudaSuccess) return PA_ERR_CUDA;
+        if (cap != cudaStreamCaptureStatusNone) {
+            *cnt = reinterpret_cast<int*>(spare);
+            return cudaMemsetAsync(spare, 0, bytes, stream) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+        }
+        plan->retired.reserve(plan->retired.size() + 1);
+        const size_t want = std::max(bytes, 2 * plan->cnt_bytes);
+        int* c = nullptr;
+        if (cudaMalloc(reinterpret_cast<void**>(&c), want) != cudaSuccess) {
+            cudaGetLastError();
+            return PA_ERR_CUDA;
+        }
+        if (cudaMemsetAsync(c, 0, want, stream) != cudaSuccess) {
+            cudaFree(c);
+            return PA_ERR_CUDA;
+        }
+        if (plan->cnt) plan->retired.push_back(plan->cnt);  // a captured graph may use them
+        plan->cnt = c;
+        plan->cnt_bytes = want;
+    }
+    *cnt = plan->cnt;
     return PA_OK;
 }
 
@@ -442,7 +474,7 @@ pa_status decode_impl(const void* q, const int32_t* q_start, int T, int nq, cons
                       int num_blocks, int max_seq_len, float scale, pa_dtype kv_dtype, void* out,
                       pa_dtype out_dtype, pa_plan** plan_inout, struct CUstream_st* stream_,
                       const void* k_new = nullptr, const void* v_new = nullptr, int window = 0,
-                      int sinks = 0) {
+                      int sinks = 0) try {
     if (!q || !k_pool || !v_pool || !block_tables || !seq_lens || !out || !plan_inout)
         return PA_ERR_NULL;
     if (k_new && (!aligned16(k_new) || !aligned16(v_new))) return PA_ERR_ALIGN;
@@ -545,7 +577,6 @@ pa_status decode_impl(const void* q, const int32_t* q_start, int T, int nq, cons
             const size_t need = 64 + pa::prefill_window_bytes(B, Hq, Hkv, T, vis_len, plan->num_sms);
             const pa_status st = grow_workspace(plan, need, stream);
             if (st != PA_OK) return st;
-            plan->cnt_clean = std::min(plan->cnt_clean, plan->ws_bytes - need);
             if (plan->ev_start) cudaEventRecord(plan->ev_start, stream);
             const cudaError_t e = pa::launch_prefill_window(
                 kmap, vmap, q, T, q_start, block_tables, seq_lens, out, plan->err, B, Hq, Hkv,
@@ -572,10 +603,8 @@ pa_status decode_impl(const void* q, const int32_t* q_start, int T, int nq, cons
                 if (cudaMalloc(&plan->ws, need) != cudaSuccess) return PA_ERR_CUDA;
                 if (cudaMemset(plan->ws, 0, need) != cudaSuccess) return PA_ERR_CUDA;
                 plan->ws_bytes = need;
-                plan->cnt_clean = need;
             }
             part = reinterpret_cast<float*>(static_cast<char*>(plan->ws) + 64);
-            plan->cnt_clean = std::min(plan->cnt_clean, plan->ws_bytes - need);
         }
         if (plan->ev_start) cudaEventRecord(plan->ev_start, stream);
         const cudaError_t e =
@@ -713,27 +742,16 @@ pa_status decode_impl(const void* q, const int32_t* q_start, int T, int nq, cons
         if (cudaMalloc(&plan->ws, need_ws) != cudaSuccess) return PA_ERR_CUDA;
         if (cudaMemset(plan->ws, 0, need_ws) != cudaSuccess) return PA_ERR_CUDA;  // piece counter = 0
         plan->ws_bytes = need_ws;
-        plan->cnt_clean = need_ws;
     }
     char* ws = static_cast<char*>(plan->ws);
     int* meta = reinterpret_cast<int*>(ws);
     float* ml = reinterpret_cast<float*>(ws + gr.meta_bytes);
     float* acc = reinterpret_cast<float*>(ws + gr.meta_bytes + gr.ml_bytes);
-    // The segment counters of the fused merge sit at the end of the
-    // workspace. A fused call leaves them zero; the plan tracks how many bytes
-    // at the end are known to be zero (all of a fresh workspace, less what
-    // any call's partials have overwritten) and clears the counters when a
-    // call needs more than that.
     int* cnt = nullptr;
     if (L.fused) {
-        cnt = reinterpret_cast<int*>(ws + plan->ws_bytes - gr.cnt_bytes);
-        if (plan->cnt_clean < gr.cnt_bytes) {
-            if (cudaMemsetAsync(cnt, 0, gr.cnt_bytes, stream) != cudaSuccess) return PA_ERR_CUDA;
-            plan->cnt_clean = gr.cnt_bytes;
-        }
+        const pa_status st = fused_counters(plan, gr.cnt_bytes, ws + plan->ws_bytes - gr.cnt_bytes, stream, &cnt);
+        if (st != PA_OK) return st;
     }
-    plan->cnt_clean = std::min(plan->cnt_clean,
-                               plan->ws_bytes - (gr.meta_bytes + gr.ml_bytes + gr.acc_bytes));
 
     const int rows = num_blocks * Hkv;
     MapKey kk{k_pool, rows, D, block_size}, vk{v_pool, rows, D, block_size};
@@ -803,6 +821,8 @@ pa_status decode_impl(const void* q, const int32_t* q_start, int T, int nq, cons
     plan->last_blocks = L.blocks;
     plan->last_warps = gr.NW;
     return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+} catch (...) {  // host memory
+    return PA_ERR_CUDA;
 }
 
 }  // namespace
@@ -848,13 +868,9 @@ pa_status pa_decode_window(const void* q, const void* k_pool, const void* v_pool
                            void* out, pa_dtype out_dtype, pa_plan** plan_inout,
                            struct CUstream_st* stream) {
     if (window < 1 || sinks < 0) return PA_ERR_SHAPE;
-    try {
-        return decode_impl(q, nullptr, B, 1, k_pool, v_pool, block_tables, max_blocks, seq_lens, B,
-                           Hq, Hkv, D, block_size, num_blocks, max_seq_len, scale, kv_dtype, out,
-                           out_dtype, plan_inout, stream, nullptr, nullptr, window, sinks);
-    } catch (...) {  // host memory
-        return PA_ERR_CUDA;
-    }
+    return decode_impl(q, nullptr, B, 1, k_pool, v_pool, block_tables, max_blocks, seq_lens, B,
+                       Hq, Hkv, D, block_size, num_blocks, max_seq_len, scale, kv_dtype, out,
+                       out_dtype, plan_inout, stream, nullptr, nullptr, window, sinks);
 }
 
 pa_status pa_prefill_window(const void* q, const int32_t* q_start, int num_queries, int max_q,
@@ -866,14 +882,9 @@ pa_status pa_prefill_window(const void* q, const int32_t* q_start, int num_queri
     if (!q_start) return PA_ERR_NULL;
     // The tiles' row maxima are taken before the scale: it must be positive.
     if (window < 1 || sinks < 0 || !(scale > 0.f) || B > pa::kMaxGridYZ) return PA_ERR_SHAPE;
-    try {
-        return decode_impl(q, q_start, num_queries, max_q, k_pool, v_pool, block_tables, max_blocks,
-                           seq_lens, B, Hq, Hkv, D, block_size, num_blocks, max_seq_len, scale,
-                           kv_dtype, out, out_dtype, plan_inout, stream, nullptr, nullptr, window,
-                           sinks);
-    } catch (...) {  // host memory
-        return PA_ERR_CUDA;
-    }
+    return decode_impl(q, q_start, num_queries, max_q, k_pool, v_pool, block_tables, max_blocks,
+                       seq_lens, B, Hq, Hkv, D, block_size, num_blocks, max_seq_len, scale, kv_dtype,
+                       out, out_dtype, plan_inout, stream, nullptr, nullptr, window, sinks);
 }
 
 pa_status pa_copy_blocks(void* k_pool, void* v_pool, const int32_t* copy_src,
@@ -935,6 +946,7 @@ pa_status pa_free(pa_plan* plan) {
     DeviceGuard guard(plan->device);
     pa_status st = PA_OK;
     if (plan->ws && cudaFree(plan->ws) != cudaSuccess) st = PA_ERR_CUDA;
+    if (plan->cnt && cudaFree(plan->cnt) != cudaSuccess) st = PA_ERR_CUDA;
     for (void* p : plan->retired)
         if (cudaFree(p) != cudaSuccess) st = PA_ERR_CUDA;
     if (plan->err && cudaFree(plan->err) != cudaSuccess) st = PA_ERR_CUDA;

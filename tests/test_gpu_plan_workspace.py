@@ -1,0 +1,74 @@
+"""GPU: what a plan's memory holds from call to call, and for how long. Calls of
+every kind share a plan's workspace in any order, among them graphs captured
+earlier and replayed in between; memory that a later call outgrows."""
+
+import pytest
+import torch
+
+import paged_kv_cache_202_gb300 as pa
+from test_gpu_window import Case
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    import __graft_entry__
+    __graft_entry__.build()
+
+
+def decode(c, plan, out=None):
+    """pa_decode of a case whose window covers its sequences."""
+    d = c.d
+    if out is None:
+        out = torch.full(c.q.shape, 7.5, dtype=torch.bfloat16, device="cuda")
+    pa.pa_decode(d["q"], d["k"], d["v"], d["table"], d["lens"], c.scale, out, max(c.lens), plan)
+    return out
+
+
+def captured(call):
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        call()
+    return g
+
+
+def test_fused_merges_between_replays_of_a_windowed_graph():
+    # The fused merge counts partials in memory that every call leaves zero. A
+    # windowed graph that is replayed in between must not write there.
+    few = Case([3000, 2500, 700, 40], Hq=16, Hkv=2, W=5000, S=0, seed=4).upload()
+    c = Case([5000, 4500], [32, 32], W=4096, S=4, seed=1).upload()
+    plan = c.plan
+    out = torch.zeros(c.q.shape, dtype=torch.bfloat16, device="cuda")
+    rows = set(range(0, c.T, 7))
+    decode(few, plan)
+    plan.set_merge(pa.PA_MERGE_FUSED)
+    few.compare(decode(few, plan))
+    c.run(prefill=True, out=out)
+    g = captured(lambda: c.run(prefill=True, out=out))
+    for _ in range(3):
+        few.compare(decode(few, plan))
+        g.replay()
+    few.compare(decode(few, plan))
+    assert plan.last_device_error() == 0
+    c.check(out, prefill=True, rows=rows)
+
+
+def test_a_captured_fused_merge_between_windowed_calls():
+    few = Case([3000, 2500, 700, 40], Hq=16, Hkv=2, W=5000, S=0, seed=4).upload()
+    c = Case([5000, 4500], [32, 32], W=4096, S=4, seed=1).upload()
+    plan = c.plan
+    res = torch.zeros(few.q.shape, dtype=torch.bfloat16, device="cuda")
+    c.run(prefill=True)
+    decode(few, plan)
+    plan.set_merge(pa.PA_MERGE_FUSED)
+    g = captured(lambda: decode(few, plan, res))    # the plan's first fused call
+    for _ in range(2):
+        c.check(c.run(prefill=True), prefill=True, rows={0, 40})
+        res.fill_(7.5)
+        g.replay()
+        torch.cuda.synchronize()
+        few.compare(res)
+        few.compare(decode(few, plan))
+    assert plan.last_device_error() == 0
