@@ -318,8 +318,8 @@ struct pa_plan {
     int* cnt = nullptr;    // the fused merge's segment counters, zero between calls
     size_t cnt_bytes = 0;
     int last_path = 0, last_blocks = 0, last_warps = 0;
-    // After a windowed call, workspaces that a call outgrows are kept until
-    // pa_free: a captured graph may still use them.
+    // After a windowed call, or a captured one, workspaces that a call outgrows
+    // are kept until pa_free: the graph may still use them.
     bool keep = false;
     std::vector<void*> retired;
     cudaEvent_t ev_start = nullptr, ev_stop = nullptr;
@@ -369,6 +369,13 @@ pa_status pa_append_kv(const void* k_new, const void* v_new, void* k_pool, void*
 }
 
 namespace {
+
+// A call on a stream that is being captured: its graph uses the plan's memory
+// from now on.
+void note_capture(pa_plan* plan, cudaStream_t stream) {
+    cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
+    if (cudaStreamIsCapturing(stream, &cap) == cudaSuccess && cap != cudaStreamCaptureStatusNone) plan->keep = true;
+}
 
 // Gives up the plan's workspace for a larger one: freed, or kept (see pa_plan).
 void drop_workspace(pa_plan* plan) {
@@ -596,7 +603,7 @@ pa_status decode_impl(const void* q, const int32_t* q_start, int T, int nq, cons
             if (window > 0) {
                 const pa_status st = grow_workspace(plan, need, stream);
                 if (st != PA_OK) return st;
-            } else if (plan->ws_bytes < need) {
+            } else if (note_capture(plan, stream); plan->ws_bytes < need) {
                 drop_workspace(plan);
                 plan->ws = nullptr;
                 plan->ws_bytes = 0;
@@ -735,7 +742,7 @@ pa_status decode_impl(const void* q, const int32_t* q_start, int T, int nq, cons
     if (L.win) {
         const pa_status st = grow_workspace(plan, need_ws, stream);
         if (st != PA_OK) return st;
-    } else if (plan->ws_bytes < need_ws) {
+    } else if (note_capture(plan, stream); plan->ws_bytes < need_ws) {
         drop_workspace(plan);
         plan->ws = nullptr;
         plan->ws_bytes = 0;

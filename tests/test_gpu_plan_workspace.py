@@ -72,3 +72,30 @@ def test_a_captured_fused_merge_between_windowed_calls():
         few.compare(res)
         few.compare(decode(few, plan))
     assert plan.last_device_error() == 0
+
+
+@pytest.mark.parametrize("multi", [False, True])
+def test_graph_replay_of_plain_calls_outlives_a_growing_plan(multi):
+    # A captured pa_decode, or pa_decode_multi with its keys split over blocks,
+    # and a larger call afterwards: the graph's memory stays its own.
+    ns = [6, 6] if multi else None
+    c = Case([3000, 2000], ns, W=5000, S=0, seed=1).upload()
+    out = torch.zeros(c.q.shape, dtype=torch.bfloat16, device="cuda")
+
+    def call():
+        if not multi:
+            return decode(c, c.plan, out)
+        d = c.d
+        pa.pa_decode_multi(d["q"], d["start"], d["k"], d["v"], d["table"], d["lens"], c.scale, out, 6, 3000, c.plan)
+
+    call()
+    g = captured(call)
+    big = Case([2500] * 40, Hq=32, Hkv=8, W=5000, S=0, seed=2).upload()
+    decode(big, c.plan)
+    other = torch.randn(64 << 20, device="cuda")      # whatever was freed may be taken
+    torch.cuda.synchronize()
+    out.zero_()
+    g.replay()
+    torch.cuda.synchronize()
+    c.check(out, prefill=multi)
+    assert bool(torch.isfinite(other).all())
