@@ -146,8 +146,11 @@ pa_status pa_append_kv(const void* k_new, const void* v_new, void* k_pool, void*
  *   out           device, [B][Hq][D] out_dtype (bf16 rounded to nearest even)
  *   plan_inout    in/out: *plan_inout == NULL makes the library create a plan
  *                 (device workspace allocation, the only allocation); a plan
- *                 is reused by later calls and grows its workspace only when
- *                 a call needs more. Release it with pa_free. A call that
+ *                 is reused by later calls and grows its workspace, to twice
+ *                 its size at least, only when a call needs more. Once a call
+ *                 of the plan has been captured, memory that a later call
+ *                 outgrows is kept until pa_free, so that the graph stays
+ *                 valid. Release a plan with pa_free. A call that
  *                 returns an argument error (PA_ERR_NULL, _SHAPE, _DTYPE,
  *                 _BLOCK_SIZE, _ALIGN) creates no plan and launches nothing.
  *
@@ -671,9 +674,7 @@ pa_status pa_qk_rope_append(const void* q, int64_t q_stride, const void* k, int6
  * pa_decode's split kernels and the plan's workspace. Calls on one plan must be
  * ordered on the device (one stream, or events). A call that has to create the
  * plan or needs a larger workspace during a stream capture returns
- * PA_ERR_WORKSPACE: make the call once before capturing it. Once a windowed
- * call has used the plan's workspace, memory that a later call outgrows is kept
- * until pa_free, so graphs captured with the plan stay valid.
+ * PA_ERR_WORKSPACE: make the call once before capturing it.
  */
 pa_status pa_decode_window(const void* q, const void* k_pool, const void* v_pool,
                            const int32_t* block_tables, int max_blocks, const int32_t* seq_lens,

@@ -31,6 +31,7 @@ constexpr int kDynMidMaxRows = 2048;       // ... while the merge has at most th
 constexpr int kMergeRowsPerSm = 16;        // rows one SM merges at once with 4 warps per row
 constexpr int kMinPagesPerWarp = 4;
 constexpr int kHeadSlice = 16;             // query heads per kv unit on the tensor-core path
+constexpr size_t kMinWorkspace = 1 << 20;  // a plan's first workspace, at least
 
 struct MapKey {
     const void* ptr = nullptr;
@@ -318,9 +319,9 @@ struct pa_plan {
     int* cnt = nullptr;    // the fused merge's segment counters, zero between calls
     size_t cnt_bytes = 0;
     int last_path = 0, last_blocks = 0, last_warps = 0;
-    // After a windowed call, or a captured one, workspaces that a call outgrows
-    // are kept until pa_free: the graph may still use them.
-    bool keep = false;
+    // Whether a call was captured: memory that a later call outgrows is then kept
+    // until pa_free, since the graph may still use it.
+    bool captured = false;
     std::vector<void*> retired;
     cudaEvent_t ev_start = nullptr, ev_stop = nullptr;
     MapKey kkey, vkey;
@@ -370,52 +371,63 @@ pa_status pa_append_kv(const void* k_new, const void* v_new, void* k_pool, void*
 
 namespace {
 
-// A call on a stream that is being captured: its graph uses the plan's memory
-// from now on.
-void note_capture(pa_plan* plan, cudaStream_t stream) {
+// Gives up memory of the plan that a larger piece replaces. After a captured call
+// it is kept until pa_free, since the graph may use it; else it is freed (which
+// waits for the work in flight).
+void give_up(pa_plan* plan, void* memory) {
+    if (!memory) return;
+    if (plan->captured) plan->retired.push_back(memory);  // into space reserved before
+    else cudaFree(memory);
+}
+
+// Whether the stream is being captured; noted in the plan, whose memory a graph
+// uses from then on.
+cudaError_t note_capture(pa_plan* plan, cudaStream_t stream, bool* capturing) {
     cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
-    if (cudaStreamIsCapturing(stream, &cap) == cudaSuccess && cap != cudaStreamCaptureStatusNone) plan->keep = true;
+    const cudaError_t e = cudaStreamIsCapturing(stream, &cap);
+    *capturing = e == cudaSuccess && cap != cudaStreamCaptureStatusNone;
+    plan->captured |= *capturing;
+    return e;
 }
 
-// Gives up the plan's workspace for a larger one: freed, or kept (see pa_plan).
-void drop_workspace(pa_plan* plan) {
-    if (!plan->ws) return;
-    if (!plan->keep) {
-        cudaFree(plan->ws);
-        return;
-    }
-    try {
-        plan->retired.push_back(plan->ws);
-    } catch (...) {
-        // No host memory for the list: the block stays allocated for good,
-        // which a graph that uses it survives.
-    }
-}
-
-// Workspace of at least `need` bytes for a windowed call. Memory that a graph
-// captured with this plan may still use stays allocated until pa_free; during
-// a capture nothing can be allocated, and the call is refused instead.
-pa_status grow_workspace(pa_plan* plan, size_t need, cudaStream_t stream) {
-    plan->keep = true;
+// Workspace of at least `need` bytes. It grows to twice its size at least: sizes
+// that creep up from step to step allocate seldom, and what captured plans keep
+// of outgrown memory is less than the workspace itself. During a capture a
+// windowed call that needs more is refused; the others try (a relaxed capture
+// lets them).
+pa_status grow_workspace(pa_plan* plan, size_t need, cudaStream_t stream, bool windowed) {
+    bool capturing = false;
+    const cudaError_t status = note_capture(plan, stream, &capturing);
     if (plan->ws_bytes >= need) return PA_OK;
-    cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
-    if (cudaStreamIsCapturing(stream, &cap) != cudaSuccess) return PA_ERR_CUDA;
-    if (cap != cudaStreamCaptureStatusNone) return PA_ERR_WORKSPACE;
+    if (windowed && status != cudaSuccess) return PA_ERR_CUDA;
+    if (windowed && capturing) return PA_ERR_WORKSPACE;
     plan->retired.reserve(plan->retired.size() + 1);
     void* ws = nullptr;
-    if (cudaMalloc(&ws, need) != cudaSuccess) {
+    size_t want = std::max({need, 2 * plan->ws_bytes, kMinWorkspace});
+    cudaError_t e = cudaMalloc(&ws, want);
+    if (e != cudaSuccess && !capturing) {  // short of memory: no more than it takes,
+        want = need;
+        e = cudaMalloc(&ws, want);
+        if (e != cudaSuccess && plan->ws && !plan->captured) {  // in place of the old
+            cudaFree(plan->ws);
+            plan->ws = nullptr;
+            plan->ws_bytes = 0;
+            e = cudaMalloc(&ws, want);
+        }
+    }
+    if (e != cudaSuccess) {
         cudaGetLastError();
         return PA_ERR_CUDA;
     }
-    // Zeroed in stream order (the piece counter starts at zero); the old
-    // memory is not touched, so calls in flight on it go on.
-    if (cudaMemsetAsync(ws, 0, need, stream) != cudaSuccess) {
+    // The split kernels' counters start at zero.
+    e = capturing ? cudaMemset(ws, 0, want) : cudaMemsetAsync(ws, 0, want, stream);
+    if (e != cudaSuccess) {
         cudaFree(ws);
         return PA_ERR_CUDA;
     }
-    if (plan->ws) plan->retired.push_back(plan->ws);
+    give_up(plan, plan->ws);
     plan->ws = ws;
-    plan->ws_bytes = need;
+    plan->ws_bytes = want;
     return PA_OK;
 }
 
@@ -425,10 +437,10 @@ pa_status grow_workspace(pa_plan* plan, size_t need, cudaStream_t stream) {
 // fused call, in which nothing can be allocated, takes `spare` instead (the end
 // of the workspace) and clears it in the graph.
 pa_status fused_counters(pa_plan* plan, size_t bytes, char* spare, cudaStream_t stream, int** cnt) {
+    bool capturing = false;
+    if (note_capture(plan, stream, &capturing) != cudaSuccess) return PA_ERR_CUDA;
     if (plan->cnt_bytes < bytes) {
-        cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
-        if (cudaStreamIsCapturing(stream, &cap) != cudaSuccess) return PA_ERR_CUDA;
-        if (cap != cudaStreamCaptureStatusNone) {
+        if (capturing) {
             *cnt = reinterpret_cast<int*>(spare);
             return cudaMemsetAsync(spare, 0, bytes, stream) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
         }
@@ -443,7 +455,7 @@ pa_status fused_counters(pa_plan* plan, size_t bytes, char* spare, cudaStream_t 
             cudaFree(c);
             return PA_ERR_CUDA;
         }
-        if (plan->cnt) plan->retired.push_back(plan->cnt);  // a captured graph may use them
+        give_up(plan, plan->cnt);
         plan->cnt = c;
         plan->cnt_bytes = want;
     }
@@ -582,7 +594,7 @@ pa_status decode_impl(const void* q, const int32_t* q_start, int T, int nq, cons
         const int64_t nqq = std::min<int64_t>(nq, T);
         if (window > 0 && window_items(B, Hq, Hkv, nqq, vis_len, plan->num_sms)) {
             const size_t need = 64 + pa::prefill_window_bytes(B, Hq, Hkv, T, vis_len, plan->num_sms);
-            const pa_status st = grow_workspace(plan, need, stream);
+            const pa_status st = grow_workspace(plan, need, stream, true);
             if (st != PA_OK) return st;
             if (plan->ev_start) cudaEventRecord(plan->ev_start, stream);
             const cudaError_t e = pa::launch_prefill_window(
@@ -600,17 +612,8 @@ pa_status decode_impl(const void* q, const int32_t* q_start, int T, int nq, cons
         float* part = nullptr;
         if (splits > 1) {
             const size_t need = 64 + pa::prefill_split_bytes(B, Hq, Hkv, nqq, splits);
-            if (window > 0) {
-                const pa_status st = grow_workspace(plan, need, stream);
-                if (st != PA_OK) return st;
-            } else if (note_capture(plan, stream); plan->ws_bytes < need) {
-                drop_workspace(plan);
-                plan->ws = nullptr;
-                plan->ws_bytes = 0;
-                if (cudaMalloc(&plan->ws, need) != cudaSuccess) return PA_ERR_CUDA;
-                if (cudaMemset(plan->ws, 0, need) != cudaSuccess) return PA_ERR_CUDA;
-                plan->ws_bytes = need;
-            }
+            const pa_status st = grow_workspace(plan, need, stream, window > 0);
+            if (st != PA_OK) return st;
             part = reinterpret_cast<float*>(static_cast<char*>(plan->ws) + 64);
         }
         if (plan->ev_start) cudaEventRecord(plan->ev_start, stream);
@@ -738,17 +741,9 @@ pa_status decode_impl(const void* q, const int32_t* q_start, int T, int nq, cons
     L.blocks = gr.blocks;
 
     // Workspace: metadata, partial (m, l), partial value sums.
-    const size_t need_ws = gr.workspace_bytes();
-    if (L.win) {
-        const pa_status st = grow_workspace(plan, need_ws, stream);
+    {
+        const pa_status st = grow_workspace(plan, gr.workspace_bytes(), stream, L.win);
         if (st != PA_OK) return st;
-    } else if (note_capture(plan, stream); plan->ws_bytes < need_ws) {
-        drop_workspace(plan);
-        plan->ws = nullptr;
-        plan->ws_bytes = 0;
-        if (cudaMalloc(&plan->ws, need_ws) != cudaSuccess) return PA_ERR_CUDA;
-        if (cudaMemset(plan->ws, 0, need_ws) != cudaSuccess) return PA_ERR_CUDA;  // piece counter = 0
-        plan->ws_bytes = need_ws;
     }
     char* ws = static_cast<char*>(plan->ws);
     int* meta = reinterpret_cast<int*>(ws);

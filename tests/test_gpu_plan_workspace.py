@@ -73,7 +73,6 @@ def test_a_captured_fused_merge_between_windowed_calls():
         few.compare(decode(few, plan))
     assert plan.last_device_error() == 0
 
-
 @pytest.mark.parametrize("multi", [False, True])
 def test_graph_replay_of_plain_calls_outlives_a_growing_plan(multi):
     # A captured pa_decode, or pa_decode_multi with its keys split over blocks,
@@ -99,3 +98,39 @@ def test_graph_replay_of_plain_calls_outlives_a_growing_plan(multi):
     torch.cuda.synchronize()
     c.check(out, prefill=multi)
     assert bool(torch.isfinite(other).all())
+
+
+@pytest.mark.parametrize("after_capture", [False, True])
+def test_growing_calls_keep_a_bounded_amount_of_memory(after_capture):
+    # Rows that creep up, in calls that each need over 20 MB: what is kept
+    # stays within a few times of what the largest of them needs.
+    T = 64 * 72
+    c = Case([6000], [T], Hq=4, Hkv=1, W=4096, S=4, seed=3).upload()
+    out = torch.zeros(c.q.shape, dtype=torch.bfloat16, device="cuda")
+    starts = [torch.tensor([0, n], dtype=torch.int32, device="cuda") for n in range(64, T + 1, 64)]
+
+    def call(start, n):
+        d = c.d
+        pa.pa_prefill_window(d["q"][:n], start, d["k"], d["v"], d["table"], d["lens"], c.scale, c.W, c.S,
+                             out[:n], n, 6000, plan)
+
+    pa.pa_debug_set_prefill_kernel(pa.PA_PREFILL_TWO_TILE)
+    try:
+        plan = c.plan
+        call(starts[0], 64)
+        g = captured(lambda: call(starts[0], 64)) if after_capture else None
+        torch.cuda.synchronize()
+        free = torch.cuda.mem_get_info()[0]
+        for i, start in enumerate(starts):
+            call(start, 64 * (i + 1))
+        torch.cuda.synchronize()
+        grown = free - torch.cuda.mem_get_info()[0]
+    finally:
+        pa.pa_debug_set_prefill_kernel(pa.PA_PREFILL_AUTO)
+    assert grown < 100 << 20
+    c.check(out, prefill=True, rows=set(range(0, T, 397)) | {T - 1})
+    if g is not None:
+        torch.cuda.synchronize()
+        g.replay()
+        torch.cuda.synchronize()
+        assert plan.last_device_error() == 0
