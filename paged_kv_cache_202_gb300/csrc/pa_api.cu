@@ -736,7 +736,7 @@ pa_status decode_impl(const void* q, const int32_t* q_start, int T, int nq, cons
     pa::SplitGrid gr = pa::split_grid(sh, B, D, block_size,
                                       static_cast<int64_t>(q_start ? T : B) * Hq,
                                       plan->num_sms, per_sm, true, 0,
-                                      plan->sched_permille, plan->sched_pages);
+                                      L.win ? -1 : plan->sched_permille, plan->sched_pages);
     if (L.fused) gr.cnt_bytes = round_up(static_cast<size_t>(B) * sh.U * 4u, 256);
     L.blocks = gr.blocks;
 

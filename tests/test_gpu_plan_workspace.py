@@ -134,3 +134,21 @@ def test_growing_calls_keep_a_bounded_amount_of_memory(after_capture):
         g.replay()
         torch.cuda.synchronize()
         assert plan.last_device_error() == 0
+
+
+def one_segment(Hq, seed=0):
+    """A windowed decode that runs the split kernels and uses the workspace."""
+    return Case([40000], Hq=Hq, Hkv=1, W=33000, S=19, seed=seed).upload()
+
+
+def test_a_forced_schedule_does_not_apply_to_windowed_calls():
+    # A schedule in small pieces needs more memory: if a windowed call took it,
+    # the capture would be refused.
+    c = one_segment(8)
+    c.check(c.run())
+    c.plan.set_schedule(500, 1)
+    out = torch.zeros(c.q.shape, dtype=torch.bfloat16, device="cuda")
+    g = captured(lambda: c.run(out=out))
+    g.replay()
+    torch.cuda.synchronize()
+    c.check(out)
