@@ -695,7 +695,9 @@ pa_status pa_decode_window(const void* q, const void* k_pool, const void* v_pool
  * may have been given back. Values of tokens that some queries of a tile see
  * and others do not must be finite.
  *
- *   q, q_start, num_queries, max_q, out   as for pa_prefill; n_b = 0 is allowed
+ *   q, q_start, num_queries, max_q, out   as for pa_prefill; n_b = 0 is allowed,
+ *              and so are rows past q_start[B] (a batch padded to num_queries),
+ *              which are left as they are
  *   window, sinks, plan_inout             as for pa_decode_window
  *   scale                                 > 0
  *

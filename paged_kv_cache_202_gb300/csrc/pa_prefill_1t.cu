@@ -716,7 +716,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 // 2^(m_s - m), o = sum_s O_s 2^(m_s - m) / l (maxima in the log2 domain); a
 // split with m_s = -inf saw no token of the row and is skipped, a NaN m_s
 // (a bad table entry) makes the row zeros. Rows of invalid sequences get
-// zeros (only multi-query calls split).
+// zeros (only multi-query calls split); rows of no sequence too, but for the
+// windowed calls, which leave the padding behind the last one alone.
 struct SplitMergeArgs {
     const float* part;
     int num_parts;
@@ -725,6 +726,7 @@ struct SplitMergeArgs {
     void* out;
     int out_bf16;
     int B, Hq, Hkv, g, Qb, tiles, splits, num_q, limit, max_q;
+    int leave_padding;
 };
 
 __global__ void __launch_bounds__(256) prefill_split_merge_kernel(const SplitMergeArgs a) {
@@ -741,6 +743,7 @@ __global__ void __launch_bounds__(256) prefill_split_merge_kernel(const SplitMer
     const size_t o0 = static_cast<size_t>(R) * kD + 4 * lane;
     const int64_t qs64 = a.q_start[b], n64 = static_cast<int64_t>(a.q_start[b + 1]) - qs64;
     const int L = a.seq_lens[b];
+    if (a.leave_padding && (t < qs64 || t >= qs64 + n64)) return;
     if (n64 < 1 || n64 > a.max_q || L < n64 || L > a.limit || qs64 < 0 || qs64 + n64 > a.num_q ||
         t < qs64 || t >= qs64 + n64) {
         // An invalid sequence (the split blocks wrote no partial for it): zeros.
@@ -867,7 +870,8 @@ cudaError_t launch_prefill_one_tile(const CUtensorMap& kmap, const CUtensorMap& 
                             static_cast<const PrefillArgs&>(a));
     if (e != cudaSuccess || splits == 1) return e;
     SplitMergeArgs m{part, a.num_parts, q_start, seq_lens, out, out_bf16, B, Hq, Hkv, a.g, a.Qb,
-                     a.tiles, splits, num_q, std::min(max_seq_len, max_blocks * block_size), max_q};
+                     a.tiles, splits, num_q, std::min(max_seq_len, max_blocks * block_size), max_q,
+                     window > 0 ? 1 : 0};
     const int64_t rows = static_cast<int64_t>(num_q) * Hq;
     prefill_split_merge_kernel<<<static_cast<unsigned>((rows + 7) / 8), 256, 0, stream>>>(m);
     return cudaGetLastError();

@@ -1,0 +1,37 @@
+"""GPU: rows of the windowed calls that are easily lost: rows behind the last
+sequence of a padded batch, which every kernel leaves as they were."""
+
+import pytest
+import torch
+
+import paged_kv_cache_202_gb300 as pa
+from test_gpu_window import Case, kernel  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    import __graft_entry__
+    __graft_entry__.build()
+
+
+@pytest.mark.parametrize("lens,ns,W", [
+    ([3000, 2000], [6, 6], 1000),             # keys split over blocks
+    ([3000, 500, 2000], [6, 0, 0], 1000),
+    ([300, 90], [70, 33], 64),
+    ([5000], [40], 4500),                     # items in parts
+    ([700] * 40, [100] * 40, 200),
+])
+def test_rows_of_the_padding_are_left_alone(lens, ns, W, kernel):  # noqa: F811
+    c = Case(lens, ns, W=W, S=4, seed=1).upload()
+    pad = 77
+    q = torch.full((c.T + pad, 8, 128), float("nan"), dtype=torch.bfloat16, device="cuda")
+    q[:c.T] = c.d["q"]
+    out = torch.full_like(q, 7.5)
+    d = c.d
+    pa.pa_prefill_window(q, d["start"], d["k"], d["v"], d["table"], d["lens"], c.scale, c.W, c.S, out, max(ns),
+                         max(lens), c.plan)
+    torch.cuda.synchronize()
+    assert bool((out[c.T:] == 7.5).all())
+    c.check(out[:c.T], prefill=True, rows=set(range(0, c.T, 1 + c.T // 40)))
