@@ -714,7 +714,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 // head), lane l on columns 4l .. 4l + 3. The two-partial rule of
 // "39 · PagedAttention" §3 over the splits: m = max_s m_s, l = sum_s l_s
 // 2^(m_s - m), o = sum_s O_s 2^(m_s - m) / l (maxima in the log2 domain); a
-// split with m_s = -inf saw no token of the row and is skipped, a NaN m_s
+// split with m_s = -inf saw no token of the row and is skipped (maxima pass over
+// NaN scores: where the sum is NaN the row is), a NaN m_s
 // (a bad table entry) makes the row zeros. Rows of invalid sequences get
 // zeros (only multi-query calls split); rows of no sequence too, but for the
 // windowed calls, which leave the padding behind the last one alone.
@@ -765,11 +766,17 @@ __global__ void __launch_bounds__(256) prefill_split_merge_kernel(const SplitMer
     }
     float acc[4] = {0.f, 0.f, 0.f, 0.f};
     float lsum = 0.f;
-    if (!poison && M != -INFINITY) {
+    if (!poison) {
         for (int sp = 0; sp < a.splits; ++sp) {
             const size_t pr = (p0 + sp) * kRows + r;
             const float m = ml[pr * 2];
-            if (m == -INFINITY) continue;
+            if (m == -INFINITY) {
+                // No token of the row; or none whose score is a number, and the
+                // row's sum, which is not one either, shows it.
+                const float l = ml[pr * 2 + 1];
+                if (l != l) acc[0] = acc[1] = acc[2] = acc[3] = l;
+                continue;
+            }
             const float w = fast_exp2(m - M);
             lsum = fmaf(ml[pr * 2 + 1], w, lsum);
             const float4 o = *reinterpret_cast<const float4*>(a.part + pr * kD + 4 * lane);

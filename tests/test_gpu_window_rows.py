@@ -1,5 +1,7 @@
 """GPU: rows of the windowed calls that are easily lost: rows behind the last
-sequence of a padded batch, which every kernel leaves as they were."""
+sequence of a padded batch, which every kernel leaves as they were, and rows
+whose query or only visible key is not a number, which show it however the work
+was split."""
 
 import pytest
 import torch
@@ -35,3 +37,32 @@ def test_rows_of_the_padding_are_left_alone(lens, ns, W, kernel):  # noqa: F811
     torch.cuda.synchronize()
     assert bool((out[c.T:] == 7.5).all())
     c.check(out[:c.T], prefill=True, rows=set(range(0, c.T, 1 + c.T // 40)))
+
+
+@pytest.mark.parametrize("lens,ns,W", [
+    ([3000, 2000], [6, 6], 1000),             # keys split over blocks
+    ([300, 190], [70, 33], 64),
+    ([5000], [40], 4500),                     # items in parts
+])
+def test_a_query_that_is_not_a_number_shows_in_the_prefill(lens, ns, W, kernel):  # noqa: F811
+    c = Case(lens, ns, W=W, S=4, seed=2)
+    c.q[3, 5] = float("nan")
+    c.upload()
+    out = c.run(prefill=True)
+    assert bool(torch.isnan(out[3, 5]).all())
+    out[3, 5] = 0
+    assert bool(torch.isfinite(out).all())
+    c.check(out, prefill=True, rows=set(range(c.T)) - {3})
+
+
+def test_the_only_key_of_a_part_shows(kernel):  # noqa: F811
+    # 769 visible indices for six queries: seven chunks in three parts, the last
+    # of one token, which only the last query sees.
+    c = Case([2001], [6], W=760, S=0, seed=3)
+    c.k[int(c.table[0, 2000 // 16]), 0, 2000 % 16] = float("nan")
+    c.upload()
+    out = c.run(prefill=True)
+    assert bool(torch.isnan(out[5, :4]).all())
+    out[5, :4] = 0
+    assert bool(torch.isfinite(out).all())
+    c.check(out, prefill=True, rows=set(range(5)))
