@@ -148,7 +148,13 @@ __global__ void __launch_bounds__(32 * (WPR > 8 ? WPR : 8)) merge_kernel(const M
             poison |= mi[k] != mi[k];   // the split kernel's poison marker
             mb = fmaxf(mb, mi[k]);      // fmaxf passes over NaN
         }
-        if (mb == -INFINITY) continue;  // nothing of the segment in this batch
+        if (mb == -INFINITY) {
+            // Nothing of the segment in this batch, or no score that is a number
+            // (maxima pass over NaN): the sums, 0 or NaN, tell.
+#pragma unroll
+            for (int k = 0; k < kBatch; ++k) l = fmaf(li[k], 0.f, l);
+            continue;
+        }
         const float fo = fast_exp2(m - mb);   // 0 while m is still -inf
         l *= fo;
 #pragma unroll
@@ -191,8 +197,11 @@ __global__ void __launch_bounds__(32 * (WPR > 8 ? WPR : 8)) merge_kernel(const M
             bad |= sm_poison[slotw + w] != 0;
         }
         if (bad || M == -INFINITY) {
+            float z = 0.f;  // NaN if a sum is, and no table entry was bad
+            if (!bad)
+                for (int w = 0; w < WPR; ++w) z = fmaf(sm_l[slotw + w], 0.f, z);
 #pragma unroll
-            for (int i = 0; i < DPL; ++i) acc[i] = 0.f;
+            for (int i = 0; i < DPL; ++i) acc[i] = z;
             store(acc);
             return;
         }

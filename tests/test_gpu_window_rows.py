@@ -66,3 +66,31 @@ def test_the_only_key_of_a_part_shows(kernel):  # noqa: F811
     out[5, :4] = 0
     assert bool(torch.isfinite(out).all())
     c.check(out, prefill=True, rows=set(range(5)))
+
+
+@pytest.mark.parametrize("lens,Hq,Hkv,W", [
+    ([300, 3000], 8, 2, 500), ([20000], 8, 1, 8191), ([40000], 8, 1, 33000), ([40000], 16, 1, 33000),
+    ([40000, 38000], 12, 1, 33000),
+])
+def test_a_query_that_is_not_a_number_shows_in_the_decode(lens, Hq, Hkv, W):
+    c = Case(lens, Hq=Hq, Hkv=Hkv, W=W, S=4, seed=2)
+    c.q[0, 3] = float("nan")
+    c.upload()
+    for dtype in (torch.bfloat16, torch.float32):
+        out = c.run(out_dtype=dtype)
+        assert bool(torch.isnan(out[0, 3]).all())
+        out[0, 3] = 0
+        assert bool(torch.isfinite(out).all())
+
+
+@pytest.mark.parametrize("Hq", [4, 12])
+def test_keys_of_a_whole_part_show_in_the_split_decode(Hq):
+    # Every key but those of the sinks' and of the last page.
+    c = Case([40000], Hq=Hq, Hkv=1, W=33000, S=16, seed=5)
+    for p in range(1, 40000 // 16 - 1):
+        if 0 <= c.table[0, p] < c.NB:
+            c.k[int(c.table[0, p])] = float("nan")
+    c.upload()
+    out = c.run()
+    assert c.plan.info()[1] > 8
+    assert bool(torch.isnan(out).all())
