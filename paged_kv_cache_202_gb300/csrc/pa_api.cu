@@ -406,9 +406,11 @@ pa_status grow_workspace(pa_plan* plan, size_t need, cudaStream_t stream, bool w
     size_t want = std::max({need, 2 * plan->ws_bytes, kMinWorkspace});
     cudaError_t e = cudaMalloc(&ws, want);
     if (e != cudaSuccess && !capturing) {  // short of memory: no more than it takes,
+        cudaGetLastError();  // (an error left behind would be taken for a launch's)
         want = need;
         e = cudaMalloc(&ws, want);
         if (e != cudaSuccess && plan->ws && !plan->captured) {  // in place of the old
+            cudaGetLastError();
             cudaFree(plan->ws);
             plan->ws = nullptr;
             plan->ws_bytes = 0;
