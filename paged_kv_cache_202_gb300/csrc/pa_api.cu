@@ -757,22 +757,7 @@ pa_status decode_impl(const void* q, const int32_t* q_start, int T, int nq, cons
         if (st != PA_OK) return st;
     }
 
-    const int rows = num_blocks * Hkv;
-    MapKey kk{k_pool, rows, D, block_size}, vk{v_pool, rows, D, block_size};
-    if (!(plan->kkey == kk)) {
-        if (!pa::encode_pool_map(&plan->kmap, k_pool, rows, D, block_size)) {
-            plan->kkey = MapKey{};
-            return PA_ERR_CUDA;
-        }
-        plan->kkey = kk;
-    }
-    if (!(plan->vkey == vk)) {
-        if (!pa::encode_pool_map(&plan->vmap, v_pool, rows, D, block_size)) {
-            plan->vkey = MapKey{};
-            return PA_ERR_CUDA;
-        }
-        plan->vkey = vk;
-    }
+    if (!pool_maps()) return PA_ERR_CUDA;
 
     pa::SplitWindowArgs a{};
     a.q = static_cast<const uint16_t*>(q);

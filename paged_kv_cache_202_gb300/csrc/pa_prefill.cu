@@ -135,12 +135,6 @@ struct PrefillArgs {
     int zero_invalid;         // 1: an invalid sequence's rows get zeros (multi-query calls)
 };
 
-__device__ __forceinline__ void st_shared_v4(uint32_t addr, uint4 v) {
-    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z),
-                 "r"(v.w)
-                 : "memory");
-}
-
 // Named barrier over `count` threads that also returns the AND of `pred`
 // over them.
 __device__ __forceinline__ bool bar_red_and(int id, int count, bool pred) {

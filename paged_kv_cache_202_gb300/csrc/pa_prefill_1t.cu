@@ -149,12 +149,6 @@ struct WindowPrefillArgs : PrefillArgs {
     int window, sinks;
 };
 
-__device__ __forceinline__ void st_shared_v4(uint32_t addr, uint4 v) {
-    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z),
-                 "r"(v.w)
-                 : "memory");
-}
-
 template <int ND>
 __device__ __forceinline__ void write_row(const PrefillArgs& a, size_t row, const float (&v)[ND],
                                           float inv, int d0) {

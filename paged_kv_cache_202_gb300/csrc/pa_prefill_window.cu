@@ -292,12 +292,6 @@ __global__ void __launch_bounds__(kItemThreads) window_items_kernel(const Args a
 
 // ------------------------------------------------------------------ attention
 
-__device__ __forceinline__ void st_shared_v4(uint32_t addr, uint4 v) {
-    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z),
-                 "r"(v.w)
-                 : "memory");
-}
-
 // Words j of threads 4 r .. 4 r + 3 become thread 4 r + j's: a 4 x 4 transpose.
 __device__ __forceinline__ void transpose4(uint32_t (&w)[4], int lane) {
 #pragma unroll
