@@ -671,7 +671,10 @@ pa_status pa_qk_rope_append(const void* q, int64_t q_stride, const void* k, int6
  * Cost: the bytes of min(L_b, window + sinks) tokens rounded to pages. A
  * sequence's pages are divided among the warps of one block or cluster, whose
  * results are merged on the chip; a few sequences with very long windows run on
- * pa_decode's split kernels and the plan's workspace. Calls on one plan must be
+ * pa_decode's split kernels and the plan's workspace. Blocks are sized for
+ * min(max_seq_len, window + sinks) tokens: shorter contexts hold them too, so a
+ * batch of lengths far below the window costs up to 3 times its bytes' time.
+ * Calls on one plan must be
  * ordered on the device (one stream, or events). A call that has to create the
  * plan or needs a larger workspace during a stream capture returns
  * PA_ERR_WORKSPACE: make the call once before capturing it.
@@ -694,6 +697,12 @@ pa_status pa_decode_window(const void* q, const void* k_pool, const void* v_pool
  * large calls) are not read for it, so blocks behind the first query's window
  * may have been given back. Values of tokens that some queries of a tile see
  * and others do not must be finite.
+ * As in pa_prefill, the probabilities are rounded to bf16 for the value product
+ * (at most 2^-8 of each; the row sum takes them unrounded): rows are 2.0e-3 to
+ * 2.3e-3 of their norm from the 64-bit result where 32-bit arithmetic and the
+ * bf16 output's rounding alone give 1.5e-3 to 1.7e-3. pa_decode_window keeps 16
+ * bits of them and has the latter. A query, or a key it sees, that is NaN makes
+ * its row NaN, here and there.
  *
  *   q, q_start, num_queries, max_q, out   as for pa_prefill; n_b = 0 is allowed,
  *              and so are rows past q_start[B] (a batch padded to num_queries),

@@ -47,10 +47,12 @@
 // What bounds it: the tensor cores are busy 68 % of the time. A tile's chain (its
 // value products 512 cycles, its next score products 512, its softmax 1200, the
 // hand-overs) is 2500 cycles a chunk against 2048 of products for both tiles, and
-// an item's end costs 2500 to 5000 more: 16384 rows of W = 4096 612 us, 1594
-// TFLOP/s (in passes apart; 690 us back to back at the power cap); 16 x 256 rows
-// of W = 2048 103 us, 1078 TFLOP/s (3.4 rounds of items in four); 4 x 4096 rows of
-// W = 128 89 us. So the code beside the softmax's loop counts: with its spills to
+// an item's end costs 2500 to 5000 more: 16384 rows of W = 4096 612 us, 1593
+// TFLOP/s (in passes apart; 655 to 662 us back to back at the power cap); 16 x 256
+// rows of W = 2048 101.5 us, 1093 TFLOP/s (3.4 rounds of items in four). With two to
+// six chunks an item its end is a third to a half of the time: 4 x 4096 rows of W =
+// 128 89 us against 49 for the bytes, of 32 heads without groups, W = 512, 192
+// against 79. So the code beside the softmax's loop counts: with its spills to
 // local memory, which does not stay in what the rings leave of L1, and O stored
 // by rows, the first took 691 us and the last 125.
 //

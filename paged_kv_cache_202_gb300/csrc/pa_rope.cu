@@ -21,10 +21,12 @@
 // bf16 head; a warp takes 4 heads at a time and goes over the heads of one
 // row, so a thread's 8 sines and cosines serve all its heads (few rows: several
 // warps share a row). The bytes bound it -- every element is read once and
-// written once: 16421 rows of 32 + 8 heads 51.9 us, 6.48 TB/s -- until the norms
-// come in, whose arithmetic fills 47 % of the issue slots: 32768 rows of 32 + 8 +
-// 8 heads 135 us, 5.96 TB/s (126 us without norms). Few rows are bound by the
-// launch and one round trip: 64 rows 2.4 us, 2.8 us with the cache write.
+// written once: 16421 rows of 32 + 8 heads 52.2 us, 6.44 TB/s (54.6 over two sets
+// of buffers in turn, of which L2 keeps less); 16384 rows of float32 99.5 us, 6.75
+// TB/s -- until the norms come in, whose arithmetic fills 47 % of the issue slots:
+// 32768 rows of 32 + 8 + 8 heads 136.8 us, 5.89 TB/s (126 us without norms), 16384
+// of float32 128.0 us, 6.29 TB/s. Few rows are bound by the launch and one round
+// trip: 64 rows 2.4 us, 2.8 us with the cache write; 2.8 and 3.3 us in float32.
 // A ring of rows in shared memory filled by bulk copies, instead of loads held in
 // registers, measured 153 us for the 32768 rows and 61 us for 16384 rows without
 // norms.

@@ -1,9 +1,9 @@
 // Paged decode attention with a sliding window and sinks (pa_decode_window):
 // one new query per sequence, over the tokens t >= L - W and t < S.
 //
-// With a window every (sequence, kv unit) segment costs about the same, min(L,
-// W + S) tokens, whatever the context's length. So the work is not cut out of
-// one long page stream (pa_split.cuh) but laid out by segment: a segment's
+// With a window every (sequence, kv unit) segment whose context is past it costs
+// the same, min(L, W + S) tokens, whatever the context's length. So the work is not
+// cut out of one long page stream (pa_split.cuh) but laid out by segment: a segment's
 // visible pages (WindowView) are divided among the warps of one block, or of a
 // cluster of up to 8 blocks where there are few segments, and the warps'
 // partial results (m, l, acc) are merged on the chip -- in shared memory, then
@@ -16,11 +16,16 @@
 // swizzle) and the warp runs the split decode's tensor-core tile on it (scores
 // S^T = K Q^T, probabilities as a bf16 pair hi + lo, O^T += V^T P^T, running
 // maximum in the log2 domain; pa_split.cuh's MmaState). Twelve such warps fill an
-// SM's shared memory, in one, two or four blocks. DRAM bounds it for many
-// segments, less the last blocks' uneven end: 64 sequences of 8 kv heads, W =
-// 1024, 43.4 us, 6.0 TB/s; 128 of 32, W = 4096, 1145 us, 7.5 TB/s. For few, the
-// latency of a chunk's copies and of the merge bounds it: one sequence of 8 kv
-// heads, W = 8191, 11.8 us, 2.9 TB/s.
+// SM's shared memory at D = 128, in one, two or four blocks; at D = 64, with half
+// the bytes a warp, registers allow 18 (15 above 8 heads a kv head). DRAM bounds it
+// for many segments, less the last blocks' uneven end: 64 sequences of 8 kv heads,
+// W = 1024, 45.4 us, 5.8 TB/s; 128 of 32, W = 4096, 1143 us, 7.5 TB/s. For few, the
+// latency of a chunk's copies and of the merge bounds it, and the SMs that a cluster
+// a segment leaves idle: one sequence of 8 kv heads, W = 8191, 64 blocks, 13.8 us,
+// 2.5 TB/s (11.5 with the pages in L2). Blocks and warps are cut for the host's
+// bound on the visible tokens, so contexts of many lengths below the window take up
+// to 3 times their bytes' time: 32 sequences of 16 to 8192 tokens, 8 kv heads, W =
+// 4096, 47 us for 119 MB.
 #include "pa_split.cuh"
 
 #include <algorithm>
