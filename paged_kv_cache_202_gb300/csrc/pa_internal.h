@@ -119,7 +119,8 @@ struct SplitQ8Args : SplitArgs {
 struct Q8Groups {
     int at[4];
     __host__ __device__ Q8Groups(int64_t P, int warps, int chunk, int cols) {  // chunk: pages; columns a unit
-        const int n = static_cast<int>((P + static_cast<int64_t>(warps) * chunk - 1) / (static_cast<int64_t>(warps) * chunk));
+        int n = static_cast<int>((P + static_cast<int64_t>(warps) * chunk - 1) / (static_cast<int64_t>(warps) * chunk));
+        if (n < 1) n = 1;  // a stream without pages has no groups, but the kernels divide by a group's
         at[0] = 0;
         at[3] = n * chunk;
         const bool two = n >= 24 && cols <= 8;

@@ -1,0 +1,61 @@
+"""Calls of the 8-bit cache at the edges of what they take."""
+
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import paged_kv_cache_202_gb300 as pa
+import q8_reference as ref
+
+pytestmark = pytest.mark.gpu
+
+
+def _i32(x):
+    return torch.tensor(list(x), dtype=torch.int32, device="cuda")
+
+
+def _q(T, Hq, D, seed):
+    return torch.randn(T, Hq, D, generator=torch.Generator("cuda").manual_seed(seed), device="cuda").to(torch.bfloat16)
+
+
+@pytest.fixture
+def plan():
+    p = pa.Plan()
+    yield p
+    p.free()
+
+
+@pytest.mark.parametrize("D,bs", [(128, 16), (64, 32)])
+@pytest.mark.parametrize("lens", [[0, 0, 0], [-1, 400, 0], [301, 302, 1 << 30]], ids=str)
+def test_decode_of_invalid_sequences_alone(lens, D, bs, plan):
+    """No sequence has a page: zero rows and the error bit, and the plan's next call is right."""
+    c = ref.Cache([300, 300, 300], 2, D, bs, seed=1)
+    q = _q(3, 8, D, 2)
+    want, tol = ref.attention(c, q, [1] * 3, 0.1)
+    for _ in range(2):
+        out = torch.full((3, 8, D), 3.0, device="cuda")
+        pa.pa_decode_q8(q, *c.args, c.dtables, _i32(lens), 0.1, out, 300, plan)
+        assert pa.pa_last_device_error(plan) == pa.PA_DEVERR_SEQ_LEN
+        assert bool((out == 0).all())
+        pa.pa_decode_q8(q, *c.args, c.dtables, c.dlens, 0.1, out, 300, plan)
+        assert pa.pa_last_device_error(plan) == 0
+        ref.check(out, want, tol)
+
+
+def test_few_queries_of_invalid_or_idle_sequences_alone(plan):
+    """The same on the decode's tiles: idle requests leave the padded rows, invalid ones get zeros."""
+    c = ref.Cache([300, 40], 2, 128, 16, seed=3)
+    q = _q(6, 8, 128, 4)
+    want, tol = ref.attention(c, q[:4], [3, 1], 0.1)
+    for start, lens, bit, left in (([0, 0, 0], [300, 40], 0, 0), ([0, 0, 0], [0, 0], 0, 0),
+                                   ([0, 3, 4], [2, 0], pa.PA_DEVERR_SEQ_LEN, 4)):
+        out = torch.full((6, 8, 128), 3.0, device="cuda")
+        pa.pa_prefill_q8(q, _i32(start), *c.args, c.dtables, _i32(lens), 0.1, out, 3, 300, plan)
+        assert pa.pa_last_device_error(plan) == bit
+        assert bool((out[:left] == 0).all()) and bool((out[left:] == 3).all())
+        pa.pa_prefill_q8(q, _i32([0, 3, 4]), *c.args, c.dtables, c.dlens, 0.1, out, 3, 300, plan)
+        assert pa.pa_last_device_error(plan) == 0
+        ref.check(out[:4], want, tol)
+        assert bool((out[4:] == 3).all())
