@@ -810,7 +810,9 @@ pa_status pa_read_kv_q8(const void* k_pool, const void* v_pool, const float* k_s
  *
  *   q         bf16 [B][Hq][D];  k_scale, v_scale  device float32, read only
  *   other arguments, limits, plan and device errors as for pa_decode (D 64 or
- *   128; the plan's forced path, merge and schedule do not apply). A call that
+ *   128; the plan's forced path, merge and schedule do not apply; B sequences of
+ *   max_seq_len tokens must have fewer than 2^31 - 2^23 pages times heads, kv
+ *   heads or groups of up to 16 query heads, else PA_ERR_SHAPE). A call that
  *   has to create the plan or needs a larger workspace during a stream capture
  *   returns PA_ERR_WORKSPACE: make the call once before capturing it. Calls on
  *   one plan must be ordered on the device.

@@ -147,7 +147,7 @@ bool split_shape(int kind, int nq, int B, int Hq, int Hkv, int D, int block_size
     s.max_pages = (static_cast<int64_t>(std::min(max_seq_len, max_blocks * block_size)) +
                    block_size - 1) / block_size;
     s.P_max = static_cast<int64_t>(B) * s.U * s.max_pages;
-    if (s.P_max > INT32_MAX) return false;
+    if (s.P_max > (kind == kSplitQ8 ? kQ8MaxPages : INT32_MAX)) return false;
 
     s.lens_bytes = round_up(static_cast<size_t>(2 * B + 1) * 4u, 1024);
     const size_t chunk = 2u * kChunkTokens * D * 2u;  // K and V of a stage

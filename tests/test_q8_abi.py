@@ -119,6 +119,11 @@ def test_prefill_refuses(lib, kw, status):
     assert _prefill(lib, **kw) == status
 
 
+def test_decode_refuses_page_streams_past_32_bits(lib):
+    """8192 sequences x 64 kv heads x 4095 pages: their number fits 32 bits, but not that and a warp's share."""
+    assert _decode(lib, B=8192, Hq=64, Hkv=64, mb=4095, maxlen=4095 * 16) == SH
+
+
 def test_binding_refuses_host_tensors():
     z = torch.zeros
     i32 = torch.int32
