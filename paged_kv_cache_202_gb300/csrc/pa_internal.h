@@ -132,7 +132,7 @@ struct Q8Groups {
 // The most pages of its stream: a group's place is reckoned in 32 bits, and its end lies
 // up to a group's pages behind the stream's, P / warps and a chunk. A grid over so many
 // pages has a block on every SM, far more than the 256 warps that this leaves room for.
-constexpr int64_t kQ8MaxPages = INT32_MAX - INT32_MAX / 256 - 256;
+constexpr int64_t kQ8MaxPages = INT32_MAX - (1 << 23);
 // Bytes of a chunk of codes, keys and values: 32 tokens of 128, 64 of 64; chunks in flight a warp.
 constexpr int kQ8ChunkBytes = 8192;
 constexpr int kQ8Stages = 2;
