@@ -154,15 +154,16 @@ pa_status attention_q8(const void* q, const int32_t* q_start, int T, int max_q, 
     // 164 / 168 / 193 / 196 us there and 268 us on the tcgen05 kernel, whose tile of 128
     // rows is mostly empty; of 4 such sequences 18.5 / 18.7 / 25.1 / 25.5 and 25 us.
     const int64_t nq = q_start ? std::min<int64_t>(max_q, T) : 0;
-    const bool split = nq * (Hq / Hkv) <= 16 && prefill_kernel_choice() == PA_PREFILL_AUTO;
+    // (A page stream too long for those, by the call's bounds, leaves it to the tcgen05 kernel.)
+    bool split = !q_start || (nq * (Hq / Hkv) <= 16 && prefill_kernel_choice() == PA_PREFILL_AUTO);
     SplitShape sh;
-    if ((!q_start || split) && !split_shape(kSplitQ8, static_cast<int>(nq), B, Hq, Hkv, D, block_size, max_blocks, max_seq_len, &sh))
-        return PA_ERR_SHAPE;
+    split = split && split_shape(kSplitQ8, static_cast<int>(nq), B, Hq, Hkv, D, block_size, max_blocks, max_seq_len, &sh);
+    if (!q_start && !split) return PA_ERR_SHAPE;
     const pa_status st = ensure_plan(plan_inout, stream, true);
     if (st != PA_OK) return st;
     pa_plan* const plan = *plan_inout;
     const float scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
-    if (!q_start || split)
+    if (split)
         return decode_split(plan, q, q_start, T, static_cast<int>(nq), k_pool, v_pool, k_scale, v_scale, tables,
                             max_blocks, seq_lens, B, Hq, Hkv, D, block_size, num_blocks, max_seq_len, scale_log2, out,
                             out_dtype == PA_BF16, sh, stream);

@@ -59,3 +59,23 @@ def test_few_queries_of_invalid_or_idle_sequences_alone(plan):
         assert pa.pa_last_device_error(plan) == 0
         ref.check(out[:4], want, tol)
         assert bool((out[4:] == 3).all())
+
+
+def test_few_queries_within_wide_bounds(plan):
+    """8192 requests of up to 65535 tokens by the call's bounds, a few of them with queries: too many
+    pages for the decode's tiles, not for the call."""
+    B, Hkv, MB = 8192, 64, 4096
+    lens, new = [300, 1, 40], [2, 1, 2]
+    c = ref.Cache(lens, Hkv, 128, 16, seed=5)
+    at = [0, 5000, B - 1]
+    tables = torch.full((B, MB), -1, dtype=torch.int32, device="cuda")
+    seq, n = torch.zeros(B, dtype=torch.int32), torch.zeros(B, dtype=torch.int32)
+    for b, L, k, row in zip(at, lens, new, c.tables):
+        tables[b, :c.MB] = torch.from_numpy(row).cuda()
+        seq[b], n[b] = L, k
+    start = torch.cat([torch.zeros(1, dtype=torch.int32), torch.cumsum(n, 0, dtype=torch.int32)]).cuda()
+    q = _q(sum(new), Hkv, 128, 6)
+    out = torch.full(q.shape, math.nan, device="cuda")
+    pa.pa_prefill_q8(q, start, *c.args, tables, seq.cuda(), 0.1, out, 2, MB * 16, plan)
+    assert pa.pa_last_device_error(plan) == 0
+    ref.check(out, *ref.attention(c, q, new, 0.1))

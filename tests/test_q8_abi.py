@@ -124,6 +124,13 @@ def test_decode_refuses_page_streams_past_32_bits(lib):
     assert _decode(lib, B=8192, Hq=64, Hkv=64, mb=4095, maxlen=4095 * 16) == SH
 
 
+@pytest.mark.skipif(torch.cuda.is_available(), reason="a GPU would run the call on its fake addresses")
+def test_prefill_of_few_queries_takes_streams_past_32_bits(lib):
+    """The same bounds are within those of pa_prefill_q8, whatever max_q: not refused, and no GPU to run on."""
+    for mq in (1, 4, 40):
+        assert _prefill(lib, B=8192, Hq=64, Hkv=64, mb=4095, maxlen=4095 * 16, mq=mq, T=40) == pa.PA_ERR_CUDA
+
+
 def test_binding_refuses_host_tensors():
     z = torch.zeros
     i32 = torch.int32
