@@ -772,7 +772,7 @@ def pa_qk_rope_append_q8(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, posi
             ("q_out", q_out, (T, Hq, D), bf, 0), ("positions", positions, (T,), _I32),
             ("q_weight", q_weight, (D,), bf), ("k_weight", k_weight, (D,), bf)))
     err = None if device_error is None else _error(what, device_error, dev)
-    if T == 0:
+    if T == 0 or B == 0:
         return
     _call(what, lib().pa_qk_rope_append_q8, dev, (
         q.data_ptr(), _rows(what, "q", q, T, Hq, D), k.data_ptr(), _rows(what, "k", k, T, Hkv, D),
@@ -802,7 +802,7 @@ def pa_read_kv_q8(k_pool: torch.Tensor, v_pool: torch.Tensor, k_scale: torch.Ten
         _refuse_q8(what, k_pool, v_pool, k_scale, v_scale, block_tables, seq_lens, q_start, dev, dims,
                    (("k_out", k_out, (T, Hkv, D), dt), ("v_out", v_out, (T, Hkv, D), dt)))
     err = None if device_error is None else _error(what, device_error, dev)
-    if T == 0:
+    if T == 0 or B == 0:
         return
     _call(what, lib().pa_read_kv_q8, dev, (
         k_pool.data_ptr(), v_pool.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), block_tables.data_ptr(), MB,

@@ -79,3 +79,20 @@ def test_few_queries_within_wide_bounds(plan):
     pa.pa_prefill_q8(q, start, *c.args, tables, seq.cuda(), 0.1, out, 2, MB * 16, plan)
     assert pa.pa_last_device_error(plan) == 0
     ref.check(out, *ref.attention(c, q, new, 0.1))
+
+
+def test_no_sequences(plan):
+    """B = 0 with padded rows is a no-op in all four calls."""
+    c = ref.Cache([40], 2, 128, 16, seed=7)
+    before = [t.view(torch.uint8).clone() for t in c.args]
+    T, none, tables = 5, _i32([]), torch.empty(0, c.MB, dtype=torch.int32, device="cuda")
+    q, k, v = _q(T, 8, 128, 1), _q(T, 2, 128, 2), _q(T, 2, 128, 3)
+    out, kr, vr = torch.full_like(q, 3.0), torch.full_like(k, 3.0), torch.full_like(v, 3.0)
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    pa.pa_qk_rope_append_q8(q, k, v, _i32([0] * T), _i32([0]), tables, none, None, *c.args, out, device_error=err)
+    pa.pa_read_kv_q8(*c.args, tables, none, _i32([0]), kr, vr, device_error=err)
+    pa.pa_prefill_q8(q, _i32([0]), *c.args, tables, none, 0.1, out, 1, 40, plan)
+    pa.pa_decode_q8(q[:0], *c.args, tables, none, 0.1, out[:0], 40, plan)
+    assert int(err) == 0 and all(bool((t == 3).all()) for t in (out, kr, vr))
+    for t, b in zip(c.args, before):
+        assert torch.equal(t.view(torch.uint8), b)
