@@ -759,6 +759,10 @@ pa_status pa_prefill_window(const void* q, const int32_t* q_start, int num_queri
  * codes that fall below the smallest normal one, 2^-6). New codes are x / scale
  * rounded to nearest even, once, from 32 bits; an x that is infinite or NaN
  * becomes the NaN code. Codes behind the last written token keep their bits.
+ * Where the block had a scale that is no power of two (a caller's own; this call
+ * makes none), codes are within 2^-22 of x of that: x times the scale's inverse,
+ * and an earlier code times the quotient of the scales, are rounded to 32 bits
+ * first, so that one next to the middle of two codes may become the other.
  *
  *   q, k, v, positions, weights, eps, rope, q_out   as for pa_qk_rope_append,
  *                 bf16 only

@@ -96,3 +96,41 @@ def test_no_sequences(plan):
     assert int(err) == 0 and all(bool((t == 3).all()) for t in (out, kr, vr))
     for t, b in zip(c.args, before):
         assert torch.equal(t.view(torch.uint8), b)
+
+
+@pytest.mark.parametrize("D,bs", [(128, 16), (64, 32)])
+def test_write_over_scales_that_are_no_powers_of_two(D, bs):
+    """A caller's larger scale stays, and every code is within half a step and 2^-22 of x (or of the earlier
+    token's value), also where x / scale is within 2^-24 of the middle of two codes; a smaller one grows to
+    a power of two."""
+    nb, Hkv = 60, 4
+    rng = np.random.default_rng(10)
+    x = torch.from_numpy(rng.uniform(1, 2, (nb, Hkv))).to(torch.bfloat16).double().numpy()
+    middle = rng.integers(8, 16, (nb, Hkv)) + 0.5   # of two neighbouring codes
+    scales = (x / middle).astype(np.float32)
+    scales[:, 1] *= np.float32(2.0 ** -12)          # too small for the new token
+    powers = 2.0 ** rng.integers(-12, 1, (nb, Hkv, D))
+    powers[..., 0] = 1
+    rows = x[..., None] * powers * rng.choice([-1.0, 1.0], (nb, Hkv, D))
+    c = ref.Cache([2] * nb, Hkv, D, bs, seed=8, slack=0)
+    blk = c.tables[:, 0]
+    for s, codes in zip(c.scales, c.codes):   # an earlier token in every block
+        s[blk] = scales
+        codes[blk, :, 0] = ref.nearest(rng.uniform(-448, 448, (nb, Hkv, D)))
+    c.upload()
+    new = torch.from_numpy(rows).to(torch.bfloat16).cuda()
+    pa.pa_qk_rope_append_q8(new, new, new, _i32([0] * nb), _i32(range(nb + 1)), c.dtables, c.dlens, None, *c.args,
+                            torch.empty_like(new))
+    need = np.vectorize(ref.scale_for)(np.abs(rows).max(-1))
+    assert bool((need[:, 1] > scales[:, 1]).all()) and bool((np.delete(need <= scales, 1, 1)).all())
+    for pool, scale, codes in zip(c.args[:2], c.args[2:], c.codes):
+        s = scale.cpu().numpy()[blk]
+        np.testing.assert_array_equal(s, np.maximum(scales, need).astype(np.float32))
+        got = ref.VALUES[pool.view(torch.uint8).cpu().numpy()[blk]]
+        old = ref.VALUES[codes[blk][:, :, 0]] * scales[..., None].astype(np.float64)
+        s = s.astype(np.float64)[..., None]
+        for i, y in ((0, old), (1, rows)):
+            assert np.all(np.abs(got[:, :, i] * s - y) <= ref.half_step(y / s * (1 + 2.0 ** -22)) * s + 2.0 ** -22 * np.abs(y))
+        keep = [h for h in range(Hkv) if h != 1]
+        np.testing.assert_array_equal(got[:, keep, 0], ref.VALUES[codes[blk]][:, keep, 0])
+        assert bool(np.isnan(got[:, :, 2:]).all())
