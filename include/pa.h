@@ -791,8 +791,9 @@ pa_status pa_qk_rope_append_q8(const void* q, int64_t q_stride, const void* k, i
 /*
  * pa_read_kv_q8 -- the keys and values of the sequences' newest tokens, read
  * back as rows: k_out and v_out [num_rows][Hkv][D] of out_dtype (bf16 or
- * float32), code times scale, rounded once. (Tokens f .. e - 1 of a sequence:
- * seq_lens[b] = e and e - f rows.)
+ * float32), code times scale as the nearest float32, and that as the nearest
+ * bf16 (powers of two: exact, but for what out_dtype has no number for). (Tokens
+ * f .. e - 1 of a sequence: seq_lens[b] = e and e - f rows.)
  *
  * Errors as for pa_qk_rope_append_q8; skipped rows are left as they are.
  */

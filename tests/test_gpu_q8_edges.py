@@ -134,3 +134,25 @@ def test_write_over_scales_that_are_no_powers_of_two(D, bs):
         keep = [h for h in range(Hkv) if h != 1]
         np.testing.assert_array_equal(got[:, keep, 0], ref.VALUES[codes[blk]][:, keep, 0])
         assert bool(np.isnan(got[:, :, 2:]).all())
+
+
+@pytest.mark.parametrize("D,bs", [(128, 16), (64, 32)])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_read_rounds_as_documented(D, bs, dtype):
+    """Code times scale to float32, and that to bf16, bit for bit, for products within 2^-24 of the middle
+    of two bf16 numbers too (what rounding once would change)."""
+    nb, Hkv = 50, 6
+    rng = np.random.default_rng(11)
+    c = ref.Cache([bs] * nb, Hkv, D, bs, seed=12, slack=0)
+    # Scales whose products with the codes of mantissa 9, 11, 13 or 15 come next to j + 1/2 for 8 bits j.
+    m = rng.choice([9, 11, 13, 15], (2, nb, Hkv))
+    f = np.rint((2 * rng.integers(128, 256, (2, nb, Hkv)) + 1) * 2.0 ** 18 / m) * 2.0 ** rng.integers(-40, -20, (2, nb, Hkv))
+    for i in range(2):
+        c.scales[i][c.tables[:, 0]] = f[i].astype(np.float32)
+    c.upload()
+    outs = [torch.full((nb * bs, Hkv, D), math.nan, dtype=dtype, device="cuda") for _ in range(2)]
+    pa.pa_read_kv_q8(*c.args, c.dtables, c.dlens, _i32(range(0, (nb + 1) * bs, bs)), *outs)
+    for i, out in enumerate(outs):
+        y = torch.cat([c.dense(b)[i].transpose(0, 1) for b in range(nb)])   # exact in 64 bits
+        assert int((y != y.float().double()).sum()) > 1000
+        assert torch.equal(out, y.float().to(dtype))
