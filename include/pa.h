@@ -733,8 +733,12 @@ pa_status pa_prefill_window(const void* q, const int32_t* q_start, int num_queri
  *   k_scale, v_scale  float32 [num_blocks][Hkv]
  * An element is its code times the scale of its block and kv head, so a block
  * of 16 tokens and 8 heads of 128 takes 32832 bytes where bf16 takes 65536.
- * Scales are finite and positive; the writing call makes powers of two, the
- * reading ones take any. The codes may be copied like other bytes
+ * Scales are finite and positive; the writing call makes powers of two from
+ * 2^-64 to 2^120, pa_read_kv_q8 takes any. The attention takes any k_scale with
+ * which the scores are finite in 32 bits, and any mix of v_scales from 2^-64 to
+ * 2^120 (sequences whose blocks' span more than 2^80 may take up to twice the
+ * time); a block with another scale (0, negative, out of range, NaN) makes the
+ * rows that see it NaN. The codes may be copied like other bytes
  * (pa_copy_blocks over the pool as bf16 of half the D); a block's scales go
  * with it.
  *

@@ -771,8 +771,14 @@ __global__ void __launch_bounds__(256) prefill_split_merge_kernel(const SplitMer
                 if (l != l) acc[0] = acc[1] = acc[2] = acc[3] = l;
                 continue;
             }
-            const float w = fast_exp2(m - M);
-            lsum = fmaf(ml[pr * 2 + 1], w, lsum);
+            const float w = fast_exp2(m - M), l = ml[pr * 2 + 1];
+            // (Far below, w may be 0 while l w counts: sums over value scales, pa_q8.cuh.)
+            if (m - M < -100.f) {
+                const float h = fast_exp2(0.5f * (m - M));
+                lsum += l * h * h;
+            } else {
+                lsum = fmaf(l, w, lsum);
+            }
             const float4 o = *reinterpret_cast<const float4*>(a.part + pr * kD + 4 * lane);
             acc[0] = fmaf(o.x, w, acc[0]);
             acc[1] = fmaf(o.y, w, acc[1]);

@@ -50,6 +50,7 @@
 // for its products, and the block frees its tensor memory.
 #include <algorithm>
 #include <cfloat>
+#include <type_traits>
 
 #include "pa.h"
 #include "pa_internal.h"
@@ -116,7 +117,7 @@ struct Layout {
     static constexpr uint32_t kTmem = kProbe + 8;
     static constexpr uint32_t kAbort = kTmem + 4;
     static constexpr uint32_t kSeq = kAbort + 4;
-    // Scales of a chunk's pages, [chunk % 2][page] (score factor, log2 vs, 1 / vs, -).
+    // Scales of a chunk's pages, [chunk % 2][page] (score factor, log2 vs, 2^24 / vs, -).
     static constexpr uint32_t kOffScale = kOffBar + 256;
     // The lengths of the ordering, then (maximum, sum) of group 1's rows.
     static constexpr uint32_t kOffRows = kOffScale + 2 * 8 * 16;
@@ -419,73 +420,85 @@ __global__ void __launch_bounds__(kThreads, 1)
             ok = __all_sync(0xffffffffu, wait_role(bars + M::kS + 8 * t, i & 1, abort_flag, a.err));
             if (!ok) break;
             tc::fence_after_sync();
-            float sv[kChunk / 2];
-            tc::ld16x2_32<64>(s_addr, *reinterpret_cast<float(*)[32]>(sv));
-            tc::ld16x2_32<64>(s_addr + 32, *reinterpret_cast<float(*)[32]>(sv + 32));
-            tc::wait_ld();
-            // Causal mask by predicate; the warp skips it when no row needs it. (Rows
-            // past the tile's queries are never stored.)
-            if (__any_sync(0xffffffffu, row_valid && c * kChunk + kChunk - 1 > pos_r)) {
-                const int last = pos_r - (c * kChunk + 64 * half);
+            // The scores' maximum, weights and sum. FAR: value scales far apart (pa_q8.cuh).
+            auto weights = [&](auto far) {
+                constexpr bool FAR = decltype(far)::value;
+                float sv[kChunk / 2];
+                tc::ld16x2_32<64>(s_addr, *reinterpret_cast<float(*)[32]>(sv));
+                tc::ld16x2_32<64>(s_addr + 32, *reinterpret_cast<float(*)[32]>(sv + 32));
+                tc::wait_ld();
+                // Causal mask by predicate; the warp skips it when no row needs it. (Rows
+                // past the tile's queries are never stored.)
+                if (__any_sync(0xffffffffu, row_valid && c * kChunk + kChunk - 1 > pos_r)) {
+                    const int last = pos_r - (c * kChunk + 64 * half);
 #pragma unroll
-                for (int j = 0; j < kChunk / 2; ++j) sv[j] = j <= last ? sv[j] : -INFINITY;
-            }
-            // Row maximum in the log2 domain, page by page (factors are positive), then
-            // the partner's half.
-            float mp[kHalfPages][2];
-#pragma unroll
-            for (int p = 0; p < kHalfPages; ++p) {
-                mp[p][0] = fmaxf(sv[p * BS], sv[p * BS + 1]);
-                mp[p][1] = fmaxf(sv[p * BS + 2], sv[p * BS + 3]);
-            }
-#pragma unroll
-            for (int j = 4; j < BS; j += 4)
+                    for (int j = 0; j < kChunk / 2; ++j) sv[j] = j <= last ? sv[j] : -INFINITY;
+                }
+                // Row maximum in the log2 domain, page by page (factors are positive), then
+                // the partner's half.
+                float mp[kHalfPages][2];
 #pragma unroll
                 for (int p = 0; p < kHalfPages; ++p) {
-                    mp[p][0] = max3(mp[p][0], sv[p * BS + j], sv[p * BS + j + 1]);
-                    mp[p][1] = max3(mp[p][1], sv[p * BS + j + 2], sv[p * BS + j + 3]);
+                    mp[p][0] = fmaxf(sv[p * BS], sv[p * BS + 1]);
+                    mp[p][1] = fmaxf(sv[p * BS + 2], sv[p * BS + 3]);
                 }
 #pragma unroll
-            for (int p = 0; p < kHalfPages; ++p) mp[p][0] = fmaf(fmaxf(mp[p][0], mp[p][1]), fac[p], off[p]);
-            float mx = fmaxf(mp[0][0], mp[1][0]);
-            if constexpr (kHalfPages == 4) mx = max3(mx, mp[2][0], mp[3][0]);
-            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-            float alpha = 1.f;
-            if (mx > m + kRaise) {
-                alpha = fast_exp2(m - mx);  // 0 while m is still -inf
-                m = mx;
-                l *= alpha;
-            }
-            const float m_use = (m == -INFINITY ? 0.f : m) - kBias;
-            if (i > 0 && __any_sync(0xffffffffu, alpha != 1.f)) rescale(o_addr, alpha);
-            // W = 2^(s' - m) (f16 pairs) over columns 32 half .. of the row; the arguments
-            // and sums two at a time, a page's sum times 1 / vs into l. In two parts, of 32
-            // of each half's 64 tokens: the first part's product runs while the second is
-            // computed.
+                for (int j = 4; j < BS; j += 4)
 #pragma unroll
-            for (int h2 = 0; h2 < 2; ++h2) {
-                uint32_t pw[16];
-#pragma unroll
-                for (int p = 0; p < 32 / BS; ++p) {
-                    const int pg = h2 * (32 / BS) + p;
-                    const uint64_t sc2 = f32x2(fac[pg], fac[pg]), of2 = f32x2(off[pg] - m_use, off[pg] - m_use);
-                    uint64_t sum[2];
-#pragma unroll
-                    for (int j = 0; j < BS / 2; ++j) {
-                        const int e = pg * BS + 2 * j;
-                        const float2 x = f32x2_split(fma_f32x2(f32x2(sv[e], sv[e + 1]), sc2, of2));
-                        const float p0 = fast_exp2(x.x), p1 = fast_exp2(x.y);
-                        sum[j & 1] = j < 2 ? f32x2(p0, p1) : add_f32x2(sum[j & 1], f32x2(p0, p1));
-                        pw[p * (BS / 2) + j] = pack_f16x2(p0, p1);
+                    for (int p = 0; p < kHalfPages; ++p) {
+                        mp[p][0] = max3(mp[p][0], sv[p * BS + j], sv[p * BS + j + 1]);
+                        mp[p][1] = max3(mp[p][1], sv[p * BS + j + 2], sv[p * BS + j + 3]);
                     }
-                    const float2 s2 = f32x2_split(add_f32x2(sum[0], sum[1]));
-                    l = fmaf(s2.x + s2.y, page[pg].z, l);
+#pragma unroll
+                for (int p = 0; p < kHalfPages; ++p) mp[p][0] = fmaf(fmaxf(mp[p][0], mp[p][1]), fac[p], off[p]);
+                float mx = fmaxf(mp[0][0], mp[1][0]);
+                if constexpr (kHalfPages == 4) mx = max3(mx, mp[2][0], mp[3][0]);
+                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+                float alpha = 1.f;
+                if (mx > m + kRaise) {
+                    alpha = fast_exp2(m - mx);  // 0 while m is still -inf
+                    if constexpr (FAR) l = q8::times_exp2(l, m - mx);
+                    else l *= alpha;
+                    m = mx;
                 }
-                tc::st16x2_16u<32>(s_addr + 16 * h2, pw);
-                tc::wait_st();
-                tc::fence_before_sync();
-                mbar_arrive(bars + M::kP + 16 * h2 + 8 * t);
-            }
+                const float m_use = (m == -INFINITY ? 0.f : m) - kBias;
+                if (i > 0 && __any_sync(0xffffffffu, alpha != 1.f)) rescale(o_addr, alpha);
+                // W = 2^(s' - m) (f16 pairs) over columns 32 half .. of the row; the arguments
+                // and sums two at a time, a page's sum times 1 / vs into l. In two parts, of 32
+                // of each half's 64 tokens: the first part's product runs while the second is
+                // computed.
+#pragma unroll
+                for (int h2 = 0; h2 < 2; ++h2) {
+                    uint32_t pw[16];
+#pragma unroll
+                    for (int p = 0; p < 32 / BS; ++p) {
+                        const int pg = h2 * (32 / BS) + p;
+                        const uint64_t sc2 = f32x2(fac[pg], fac[pg]), of2 = f32x2(off[pg] - m_use, off[pg] - m_use);
+                        uint64_t sum[2];
+#pragma unroll
+                        for (int j = 0; j < BS / 2; ++j) {
+                            const int e = pg * BS + 2 * j;
+                            const float2 x = f32x2_split(fma_f32x2(f32x2(sv[e], sv[e + 1]), sc2, of2));
+                            const float p0 = fast_exp2(x.x), p1 = fast_exp2(x.y);
+                            sum[j & 1] = j < 2 ? f32x2(p0, p1) : add_f32x2(sum[j & 1], f32x2(p0, p1));
+                            pw[p * (BS / 2) + j] = pack_f16x2(p0, p1);
+                        }
+                        const float2 s2 = f32x2_split(add_f32x2(sum[0], sum[1]));
+                        if constexpr (FAR) {
+#pragma unroll
+                            for (int j = 0; j < BS; ++j) l += fast_exp2(fmaf(sv[pg * BS + j], fac[pg], q8::kSumBias - m_use));
+                        } else {
+                            l = fmaf(s2.x + s2.y, page[pg].z, l);
+                        }
+                    }
+                    tc::st16x2_16u<32>(s_addr + 16 * h2, pw);
+                    tc::wait_st();
+                    tc::fence_before_sync();
+                    mbar_arrive(bars + M::kP + 16 * h2 + 8 * t);
+                }
+            };
+            if (__float_as_uint(off[0]) & 1u) weights(std::true_type());
+            else weights(std::false_type());
         }
         // Epilogue.
         bool fine = ok && busy && __all_sync(0xffffffffu, wait_role(bars + M::kO, 0, abort_flag, a.err));
@@ -493,7 +506,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if constexpr (PAIR) {
             if (fine) {
                 tc::fence_after_sync();
-                const float inv = 1.f / l;
+                const float inv = q8::kSumFactor / l;
 #pragma unroll
                 for (int piece = 0; piece < 2; ++piece) {
                     float o[32];
@@ -519,7 +532,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const float mt = fmaxf(r0.x, r1.x), mu = mt == -INFINITY ? 0.f : mt;
                 const float f0 = fast_exp2(r0.x - mu), f1 = fast_exp2(r1.x - mu);  // 0 without a score
                 // (Sums without a score that is a number: 0, or NaN, which shows.)
-                const float lt = (r0.x == -INFINITY ? r0.y : r0.y * f0) + (r1.x == -INFINITY ? r1.y : r1.y * f1);
+                const float lt = (r0.x == -INFINITY ? r0.y : q8::times_exp2(r0.y, r0.x - mu)) +
+                                 (r1.x == -INFINITY ? r1.y : q8::times_exp2(r1.y, r1.x - mu));
                 const uint32_t at = tmem + lane_base + 32 * t;
                 float o[32];
                 tc::ld16x2_32<64>(at + col_o(0), o);
@@ -538,7 +552,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 if (row_valid) {
                     if (!partial) {
-                        write_row(a, out_row, o, 1.f / lt, 64 * half + 32 * t);
+                        write_row(a, out_row, o, q8::kSumFactor / lt, 64 * half + 32 * t);
                     } else {
                         float* dst = part_o + static_cast<size_t>(row) * kD + 64 * half + 32 * t;
 #pragma unroll
@@ -546,7 +560,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             *reinterpret_cast<float4*>(dst + j) = make_float4(o[j], o[j + 1], o[j + 2], o[j + 3]);
                         if (t == 0 && half == 0) {
                             part_ml[2 * row] = mt;
-                            part_ml[2 * row + 1] = lt;
+                            part_ml[2 * row + 1] = lt * (1.f / q8::kSumFactor);
                         }
                     }
                 }
@@ -694,6 +708,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             // chunk k is free once the value products of chunk k - 2, whose weights
             // came after its softmax, are done.
             float ks = 1.f, vs = 1.f;
+            float top = -INFINITY, bottom = INFINITY;  // log2 of the largest and smallest value scale so far
             auto load = [&](int c) {
                 const int p = c * kPages + lane;
                 ks = vs = 1.f;
@@ -705,13 +720,26 @@ __global__ void __launch_bounds__(kThreads, 1)
             };
             load(c_beg);
             for (int k = 0; k < nk; ++k) {
-                const float f = ks * a.scale_log2, lv = fast_log2(vs), iv = 1.f / vs;
+                const float f = ks * a.scale_log2, lv = q8::log2_of(vs, ks);
+                const bool here = lane < kPages && (c_beg + k) * kPages + lane < nb;
+                float most = here ? lv : -INFINITY, least = here ? lv : INFINITY;
+#pragma unroll
+                for (int off = 4; off > 0; off >>= 1) {
+                    most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, off));
+                    least = fminf(least, __shfl_xor_sync(0xffffffffu, least, off));
+                }
+                top = fmaxf(top, __shfl_sync(0xffffffffu, most, 0));
+                bottom = fminf(bottom, __shfl_sync(0xffffffffu, least, 0));
+                // Whether they are far apart (pa_q8.cuh) goes with every page of the chunk as the last bit of
+                // its log2 vs (at most 2^-17 of it off): the softmax has no register to spare for a flag.
+                const uint32_t far = top - bottom > q8::kFarApart ? 1u : 0u;
+                const float iv = q8::kSumFactor / vs;
                 if (k + 1 < nk) load(c_beg + k + 1);
                 bool ok = k < 2 || wait_role(bars + M::kV16Empty + 8 * (k & 1), ((k >> 1) - 1) & 1, abort_flag, a.err);
                 if (!__all_sync(0xffffffffu, ok)) break;
                 if (lane < kPages)
                     st_shared_v4(base + M::kOffScale + ((k & 1) * 8 + lane) * 16,
-                                 make_uint4(__float_as_uint(f), __float_as_uint(lv), __float_as_uint(iv), 0));
+                                 make_uint4(__float_as_uint(f), (__float_as_uint(lv) & ~1u) | far, __float_as_uint(iv), 0));
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bars + M::kScale + 8 * (k & 1));
             }

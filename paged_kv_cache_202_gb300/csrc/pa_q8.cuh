@@ -1,6 +1,7 @@
 // Conversions and the row mapping shared by the kernels of the 8-bit cache.
 #pragma once
 
+#include <cfloat>
 #include <cstdint>
 
 #include "pa_internal.h"
@@ -47,6 +48,28 @@ __device__ __forceinline__ float2 f16x2_split(uint32_t h) {
 __device__ __forceinline__ float scale_for(float a) {
     const uint32_t e = (__float_as_uint(a) + 0x1fffffu) >> 23;  // one more above mantissa 1.75
     return __uint_as_float((e < 71u ? 63u : e - 8u) << 23);
+}
+
+// The value scales that the attention takes: those that pa_qk_rope_append_q8 makes. Weights
+// carry the value scale of their token, w = 2^(s + log2 vs - m), and their sum does not,
+// l = sum of w / vs = sum of 2^(s - m), which spans 2^184 against the largest w. So l is
+// taken times 2^24, between 2^-89 and 2^103 a token. While the scales of a segment lie
+// within 2^90 of one another, a token whose w is below float's range is worth less than
+// 2^-43 of l. From the first page on that lies further apart (`far`), l takes 2^(s - m)
+// itself, and is brought to another m in two steps.
+constexpr float kMinValueScale = 0x1p-64f, kMaxValueScale = 0x1p120f;
+constexpr float kFarApart = 90.f, kSumBias = 24.f, kSumFactor = 0x1p24f;
+
+// log2 of a block's value scale; NaN, which shows in the rows, for scales that are none.
+__device__ __forceinline__ float log2_of(float vs, float ks) {
+    const bool fine = vs >= kMinValueScale && vs <= kMaxValueScale && ks > 0.f && ks <= FLT_MAX;
+    return fine ? fast_log2(vs) : __int_as_float(0x7fc00000);
+}
+
+// f 2^d for a 2^d that may be below float's range while the product is not.
+__device__ __forceinline__ float times_exp2(float f, float d) {
+    const float h = fast_exp2(0.5f * d);
+    return f * h * h;
 }
 
 // The work of a call on the blocks that hold its rows. Sequence b's rows lie in at

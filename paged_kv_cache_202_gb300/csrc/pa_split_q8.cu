@@ -6,7 +6,9 @@
 //   O = sum w_t vc_t,   l = sum w_t / vs,   out = O / l:
 // the values' scales sit in the exponents, so the value product takes the codes as
 // they are, and its weights, rounded to f16, keep 11 bits relative to the largest
-// whatever the scales are; l takes them unrounded. The reference m is raised only
+// for any mix of the scales that there are (pa_q8.cuh); l takes them unrounded. The
+// output in bf16 is as near to exact arithmetic as one of 32-bit weights (1.67e-3 against
+// 1.66e-3 of it). The reference m is raised only
 // when a score exceeds it by more than 8, so that most chunks need no maximum
 // across the warp (any reference gives the same quotient); weights are taken times
 // 2^7, so that f16 holds them up to there and down to 2^-32 of the largest. Codes become
@@ -29,6 +31,7 @@
 // The scales and table entries of up to 32 pages (a batch) are read by a lane each,
 // a batch ahead, and reach the tiles by shuffles.
 #include <algorithm>
+#include <type_traits>
 
 #include "pa_q8.cuh"
 #include "pa_split.cuh"
@@ -118,10 +121,11 @@ struct Q8State {
     }
 
     // The chunk's nv tokens, of rem before the sequence's end (MQ). Lane pg0 + j holds page j's scales: the keys' times the
-    // score scale and log2 e (ksl), log2 of the values' (lvs) and its inverse (ivs).
-    template <int BS>
+    // score scale and log2 e (ksl), and log2 of the values' (lvs). FAR: value scales far apart
+    // (pa_q8.cuh).
+    template <int BS, bool FAR>
     __device__ __forceinline__ void chunk(uint32_t kst, uint32_t vst, int nv, int lane, int pg0, float ksl, float lvs,
-                                          float ivs, uint32_t qst, int nh, int rem, int nqb, int g) {
+                                          uint32_t qst, int nh, int rem, int nqb, int g) {
         if (nv < CT) {
             // Behind the end: whatever is there. No value of it may be NaN.
             for (int i = lane; i < (CT - nv) * (D / 16); i += 32)
@@ -172,12 +176,12 @@ struct Q8State {
                 }
             }
             // To the log2 domain; the end masked.
-            float inv[2];
+            float inv[2];  // 2^24 / vs
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
                 const int pg = pg0 + (sub + t * 16) / BS;
                 const float ks = __shfl_sync(0xffffffffu, ksl, pg), lv = __shfl_sync(0xffffffffu, lvs, pg);
-                inv[t] = __shfl_sync(0xffffffffu, ivs, pg);
+                inv[t] = fast_exp2(q8::kSumBias - lv);
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -219,8 +223,9 @@ struct Q8State {
                         x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
                         if (x > m[nt][j] + kRaise) {
                             const float f = fast_exp2(m[nt][j] - x);  // 0 at the segment's first tokens
+                            if constexpr (FAR) l[nt][j] = q8::times_exp2(l[nt][j], m[nt][j] - x);
+                            else l[nt][j] *= f;
                             m[nt][j] = x;
-                            l[nt][j] *= f;
 #pragma unroll
                             for (int mt = 0; mt < KS; ++mt) {
                                 o[mt][nt][j] *= f;
@@ -240,8 +245,14 @@ struct Q8State {
                     float p[4];
 #pragma unroll
                     for (int i = 0; i < 4; ++i) p[i] = fast_exp2(s[t][nt][i] - base[i & 1]);
-                    l[nt][0] = fmaf(p[0] + p[2], inv[t], l[nt][0]);
-                    l[nt][1] = fmaf(p[1] + p[3], inv[t], l[nt][1]);
+                    if constexpr (FAR) {
+                        const float lv = __shfl_sync(0xffffffffu, lvs, pg0 + (sub + t * 16) / BS) - q8::kSumBias;
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) l[nt][i & 1] += fast_exp2(s[t][nt][i] - base[i & 1] - lv);
+                    } else {
+                        l[nt][0] = fmaf(p[0] + p[2], inv[t], l[nt][0]);
+                        l[nt][1] = fmaf(p[1] + p[3], inv[t], l[nt][1]);
+                    }
                     pb[t][nt][0] = movmatrix_trans(pack_f16x2(p[0], p[1]));
                     pb[t][nt][1] = movmatrix_trans(pack_f16x2(p[2], p[3]));
                 }
@@ -266,7 +277,7 @@ struct Q8State {
         }
     }
 
-    __device__ __forceinline__ void finish(const SplitArgs& a, size_t row0, int nh, bool full, bool poison, int slot,
+    __device__ __forceinline__ void finish(const SplitArgs& a, uint32_t row0, int nh, bool full, bool poison, int slot,
                                            int lane) {
         const int dr = lane >> 2;
 #pragma unroll
@@ -279,7 +290,7 @@ struct Q8State {
                 lt += __shfl_xor_sync(0xffffffffu, lt, 16);
                 const int head = nt * 8 + 2 * (lane & 3) + j;
                 if (head >= nh) continue;
-                const float f = full ? 1.f / lt : 1.f;
+                const float f = full ? q8::kSumFactor / lt : 1.f;
                 const size_t part = static_cast<size_t>(slot) * a.GS + head, row = row0 + row_of(head, a.g, a.Hq);
 #pragma unroll
                 for (int mt = 0; mt < KS; ++mt)
@@ -457,7 +468,7 @@ __device__ __forceinline__ void q8_body(const CUtensorMap* kmap, const CUtensorM
     // ---- the batch whose pages are being copied
     const uint32_t one = elect_one();
     int cnt = 0, next = 0, kvh = 0, tbl = -1;
-    uint32_t bad = 0, badstage = 0, phase = 0;
+    uint32_t bad = 0, badstage = 0, phase = 0;  // (badstage: two stages' bits, then value scales seen, see work_on)
     float ks = 1.f, vs = 1.f;
     bool issue_done = false;
     auto open = [&] {  // false: there is none
@@ -504,10 +515,10 @@ __device__ __forceinline__ void q8_body(const CUtensorMap* kmap, const CUtensorM
     };
     // ---- the batch whose pages are being worked on
     State st;
-    float ksl = 1.f, lvs = 0.f, ivs = 1.f;
+    float ksl = 1.f, lvs = 0.f;
     int opened = 0, cb = 0, cu = 0, cp = 0, ccnt = 0, ci = 0, id = 0, end = 0;
     int p_first = 0, nh = 0, nqb = 1;
-    size_t row0 = 0;
+    uint32_t row0 = 0;
     bool poison = false;
     auto work_on = [&](float ks, float vs) {  // the next batch, with the scales of its pages
         const uint32_t r = rec + (opened & 3) * sizeof(Q8Batch);
@@ -526,18 +537,21 @@ __device__ __forceinline__ void q8_body(const CUtensorMap* kmap, const CUtensorM
                 const int first = a.q_start[cb];
                 nqb = a.q_start[cb + 1] - first;
                 nh = nqb * a.g;
-                row0 = static_cast<size_t>(first) * a.Hq + h * a.g;
+                row0 = static_cast<uint32_t>(first) * a.Hq + h * a.g;
             } else {
                 nh = min(a.GS, a.g - slice * a.GS);
-                row0 = static_cast<size_t>(cb) * a.Hq + h * a.g + slice * a.GS;
+                row0 = static_cast<uint32_t>(cb) * a.Hq + h * a.g + slice * a.GS;
             }
-            st.start(a.q + row0 * D, my_q, nh, lane, a.g, a.Hq);
+            st.start(a.q + static_cast<size_t>(row0) * D, my_q, nh, lane, a.g, a.Hq);
             p_first = cp;
             poison = false;
         }
         ksl = ks * a.scale_log2;
-        lvs = fast_log2(vs);
-        ivs = 1.f / vs;
+        lvs = q8::log2_of(vs, ks);
+        // The value scales' range so far as a bit for every 2^6.17, behind the stages' bits: one
+        // reduction, and no register of its own (the kernels of two n-tiles have none left).
+        const uint32_t now = __reduce_or_sync(0xffffffffu, lane < ccnt ? 4u << ((__float2int_rd(lvs) + 64) * 83 >> 9) : 0u);
+        badstage = (y.y ? badstage & 3u : badstage) | now;
     };
     make_batch();
     issue(0);
@@ -567,7 +581,14 @@ __device__ __forceinline__ void q8_body(const CUtensorMap* kmap, const CUtensorM
             poison = true;
         } else {
             const int rem = len[cb] - (cp + ci) * BS;
-            st.template chunk<BS>(stg, stg + kHalf, min(n * BS, rem), lane, ci, ksl, lvs, ivs, my_q, nh, rem, nqb, a.g);
+            auto chunk = [&](auto far) {
+                st.template chunk<BS, decltype(far)::value>(stg, stg + kHalf, min(n * BS, rem), lane, ci, ksl, lvs,
+                                                            my_q, nh, rem, nqb, a.g);
+            };
+            const uint32_t seen = badstage & ~3u;
+            constexpr int kSteps = static_cast<int>(q8::kFarApart) * 83 / 512 - 1;  // so many lie within kFarApart
+            if (31 - __clz(seen) - (__ffs(seen) - 1) > kSteps) chunk(std::true_type());
+            else chunk(std::false_type());
         }
         ci += n;
         __syncwarp();
@@ -687,8 +708,8 @@ __global__ void __launch_bounds__(32 * kMergeWarps, 1) q8_merge_kernel(const Spl
             mb = fmaxf(m, __shfl_sync(0xffffffffu, mb, 0));
             // No score that is a number: the sums, 0 or NaN, tell.
             const float base = mb == -INFINITY ? 0.f : mb, fo = fast_exp2(m - base), f = fast_exp2(ml.x - base);
-            l = mb == -INFINITY ? l : l * fo;
-            float lb = ml.x == -INFINITY ? ml.y : ml.y * f;
+            l = mb == -INFINITY ? l : q8::times_exp2(l, m - base);
+            float lb = ml.x == -INFINITY ? ml.y : q8::times_exp2(ml.y, ml.x - base);
 #pragma unroll
             for (int off = 4; off > 0; off >>= 1) lb += __shfl_xor_sync(0xffffffffu, lb, off);
             l += __shfl_sync(0xffffffffu, lb, 0);
@@ -724,13 +745,13 @@ __global__ void __launch_bounds__(32 * kMergeWarps, 1) q8_merge_kernel(const Spl
         for (int i = 0; i < E; ++i) acc[i] = 0.f;
         for (int j = 0; j < wpc; ++j) {
             const float mj = sm_m[warp + j], f = fast_exp2(mj - base);
-            l += mj == -INFINITY ? sm_l[warp + j] : sm_l[warp + j] * f;
+            l += mj == -INFINITY ? sm_l[warp + j] : q8::times_exp2(sm_l[warp + j], mj - base);
 #pragma unroll
             for (int i = 0; i < E; ++i) acc[i] = fmaf(sm_acc[warp + j][lane * E + i], f, acc[i]);
         }
     }
     if (col >= nh) return;
-    const float inv = 1.f / l;
+    const float inv = q8::kSumFactor / l;
 #pragma unroll
     for (int i = 0; i < E; ++i) acc[i] = bad ? 0.f : acc[i] * inv;
     const size_t row0 = MQ ? static_cast<size_t>(a.q_start[b]) * a.Hq + h * a.g
