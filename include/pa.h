@@ -812,10 +812,10 @@ pa_status pa_read_kv_q8(const void* k_pool, const void* v_pool, const float* k_s
  *
  *   out[b][h][:] = sum_t w_t v_t,  w = softmax_t(scale * q[b][h] . k_t) over
  *   t < seq_lens[b], with k_t and v_t codes times scales
- * The queries are used as they are and the codes are exact in the products; the
- * probabilities, times the values' scales, are rounded to 11 bits for the value
- * product (at most 2^-11 of each, or 2^-32 of the largest). All sums are in 32
- * bits.
+ * The queries keep their bits down to 2^-26 of a row's largest element, and the
+ * codes are exact in the products; the probabilities, times the values' scales,
+ * are rounded to 11 bits for the value product (at most 2^-11 of each, or 2^-32
+ * of the largest). All sums are in 32 bits.
  *
  *   q         bf16 [B][Hq][D];  k_scale, v_scale  device float32, read only
  *   other arguments, limits, plan and device errors as for pa_decode (D 64 or

@@ -371,8 +371,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
             most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 16));
-            sq = q8::scale_for(most);
-            const float inv = 1.f / sq;  // a power of two
+            sq = q8::scale_for(most, 1u);  // down to 2^-126: rows of any size keep the same bits
+            const float inv = 1.f / sq;    // a power of two
             const uint32_t dst = base + M::kOffQ + (PAIR ? t * kTileQ : 0) + row * 128;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {

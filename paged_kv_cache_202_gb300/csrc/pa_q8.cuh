@@ -43,11 +43,11 @@ __device__ __forceinline__ float2 f16x2_split(uint32_t h) {
     return v;
 }
 
-// The smallest power of two s with a <= 448 s, at least 2^-64 (a >= 0, finite):
+// The smallest power of two s with a <= 448 s, at least 2^-64 (2^(least - 127); a >= 0, finite):
 // 448 = 1.75 x 2^8, so s is 2^(e - 8) for a = m 2^e with m <= 1.75, else 2^(e - 7).
-__device__ __forceinline__ float scale_for(float a) {
+__device__ __forceinline__ float scale_for(float a, uint32_t least = 63u) {
     const uint32_t e = (__float_as_uint(a) + 0x1fffffu) >> 23;  // one more above mantissa 1.75
-    return __uint_as_float((e < 71u ? 63u : e - 8u) << 23);
+    return __uint_as_float((e < least + 8u ? least : e - 8u) << 23);
 }
 
 // The value scales that the attention takes: those that pa_qk_rope_append_q8 makes. Weights

@@ -84,8 +84,8 @@ struct Q8State {
                                    fmaxf(fabsf(bf16_lo(w[kk].y)), fabsf(bf16_hi(w[kk].y)))));
             a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 1));
             a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 2));
-            // 2^(e - 8) for the largest's exponent e, in [-100, 128]. (Infinities stay.)
-            const uint32_t e = max(__float_as_uint(a) >> 23, 27u);
+            // 2^(e - 8) for the largest's exponent e, at least 2^-126. (Infinities stay.)
+            const uint32_t e = max(__float_as_uint(a) >> 23, 9u);
             const float s = __uint_as_float((e - 8u) << 23), inv = __uint_as_float((262u - e) << 23);
 #pragma unroll
             for (int j = 0; j < 2; ++j) qs[nt][j] = __shfl_sync(0xffffffffu, s, 8 * (lane & 3) + 4 * j);

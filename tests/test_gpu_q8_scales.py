@@ -139,6 +139,24 @@ def test_zero_blocks_beside_large_values(plan):
         assert bool(((out.double() / 2.0 ** 69 - 1).abs() < 2.0 ** -11).all())
 
 
+@pytest.mark.parametrize("power", [-60, -100, -115, -125, -131])
+@pytest.mark.parametrize("D", [64, 128])
+def test_tiny_queries(kernel, power, D, plan):
+    """Query rows of any size keep their bits (below 2^-126 bf16's own subnormal ones) where large keys make
+    scores of them."""
+    k = min(-power - 7.0, 119.0)
+    lens, new = [300, 77, 700], [40, 3, 100]
+    c = ref.Cache(lens, 2, D, 16, seed=13, k_exp=(k - 1, k))
+    q = (_q(sum(new), 8, D, 14).float() * 2.0 ** power).to(torch.bfloat16)
+    assert float(q.abs().max()) > 0
+    want, tol = ref.attention(c, q[:3], [1] * 3, D ** -0.5)
+    ref.check(_decode(c, q[:3], plan), want, tol)
+    if D == 128:
+        for n in (new, [2, 1, 2]):
+            want, tol = ref.attention(c, q[:sum(n)], n, D ** -0.5)
+            ref.check(_prefill(c, q[:sum(n)], n, plan), want, tol)
+
+
 BAD = [(1, x) for x in (2.0 ** -65, 1e-37, 1e-40, 0.0, -1.0, 2.0 ** 121, math.inf, math.nan)] + \
       [(0, x) for x in (0.0, -1.0, math.inf, math.nan)]
 
