@@ -199,20 +199,6 @@ __device__ __forceinline__ uint4 lds_u128(uint32_t addr) {
     return v;
 }
 
-__device__ __forceinline__ float2 lds_f2(uint32_t addr) {
-    float2 v;
-    asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr));
-    return v;
-}
-
-__device__ __forceinline__ float4 lds_f4(uint32_t addr) {
-    float4 v;
-    asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
-                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-                 : "r"(addr));
-    return v;
-}
-
 // ---------------------------------------------------------------- tensor-core tile
 
 // D[16x8] += A[16x16] * B[16x8], bf16 inputs, fp32 accumulate.
@@ -251,7 +237,7 @@ __device__ __forceinline__ float fast_exp2(float x) {
     return y;
 }
 
-// log2(x) on the special-function unit: within 2^-22 of itself, exact at powers of two.
+// log2(x) on the special-function unit: off by at most 2^-22, of the result outside (0.5, 2).
 __device__ __forceinline__ float fast_log2(float x) {
     float y;
     asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
