@@ -842,7 +842,9 @@ pa_status pa_decode_q8(const void* q, const void* k_pool, const void* v_pool, co
  * codes of the new tokens are already in the pools. Precision as for
  * pa_decode_q8, and what lies below 2^-17 of a query row's largest element is
  * rounded. Values of tokens that some queries of a tile of 128 / (Hq / Hkv) see
- * and others do not must be finite.
+ * and others do not must be finite; large calls take two neighbouring tiles as
+ * one. (A weight of zero times NaN is NaN: such a value shows in the same element
+ * of the tile's other rows, and in no other tile's.)
  *
  *   q, q_start, num_queries, max_q, out   as for pa_prefill, n_b = 0 allowed
  *   plan_inout, capture                   as for pa_decode_q8

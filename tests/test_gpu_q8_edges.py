@@ -156,3 +156,26 @@ def test_read_rounds_as_documented(D, bs, dtype):
         y = torch.cat([c.dense(b)[i].transpose(0, 1) for b in range(nb)])   # exact in 64 bits
         assert int((y != y.float().double()).sum()) > 1000
         assert torch.equal(out, y.float().to(dtype))
+
+
+@pytest.mark.parametrize("kernel,tile", [(pa.PA_PREFILL_AUTO, 64), (pa.PA_PREFILL_ONE_TILE, 32),
+                                         (pa.PA_PREFILL_TWO_TILE, 64)])
+@pytest.mark.parametrize("at", [0, 31, 300, 479])
+def test_how_far_a_value_that_is_no_number_shows(kernel, tile, at, plan):
+    """In its own element of the rows that see it, at most of the same tile's (or pair's) other rows, and
+    nowhere else."""
+    L, n, g = 500, 480, 4
+    c = ref.Cache([L], 2, 128, 16, seed=15)
+    q = _q(n, 2 * g, 128, 16)
+    want, tol = ref.attention(c, q, [n], 0.1)
+    tok = L - n + at
+    c.v_pool.view(torch.uint8)[int(c.tables[0, tok // 16]), 1, tok % 16, 5] = 0x7f
+    pa.pa_debug_set_prefill_kernel(kernel)
+    try:
+        out = torch.zeros(q.shape, device="cuda")
+        pa.pa_prefill_q8(q, _i32([0, n]), *c.args, c.dtables, c.dlens, 0.1, out, n, L, plan)
+    finally:
+        pa.pa_debug_set_prefill_kernel(pa.PA_PREFILL_AUTO)
+    assert bool(torch.isnan(out[at:, g:, 5]).all())
+    out[at // tile * tile:, g:, 5] = want[at // tile * tile:, g:, 5].float()
+    ref.check(out, want, tol)
