@@ -38,6 +38,14 @@
 // blocks, whose key range may then be cut over several blocks too (splits; partials
 // and merge as in pa_prefill_1t.cu).
 //
+// A tile's next scores take the tensor memory that its weights are in, and their product is
+// issued right behind the value product that reads those. That rests on one thread's
+// products of one CTA group being carried out in the order of issue, as in the bf16
+// kernels, here for two kinds of them; the instruction set states that order for products
+// of one accumulator and shape, and this use of it is held to equal bits over repeated
+// prompts by tests. A wait between the two would leave the tensor core idle from the end
+// of each value product until its commit had been seen, twice a chunk.
+//
 // Warps:
 //   * 0-7, 8-15 (softmax groups): two threads a row, 64 of a chunk's 128 scores each;
 //     they first turn the query rows into hi and lo;
@@ -666,7 +674,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             tc::fence_after_sync();
                             issue_pv(u, k, true, 1);
                             if (u == (two ? 1 : 0)) tc::commit_if(one, bars + M::kV16Empty + 8 * (k % 2));
-                            if (k1 < nk) issue_s(u, k1);  // after the value product in issue order: W is read first
+                            if (k1 < nk) issue_s(u, k1);  // behind the value product, which reads W first (see above)
                         }
                         if (ok && k1 < nk) tc::commit_if(one, bars + M::kKEmpty + 8 * (k1 % M::kStagesK));
                     }

@@ -179,3 +179,27 @@ def test_how_far_a_value_that_is_no_number_shows(kernel, tile, at, plan):
     assert bool(torch.isnan(out[at:, g:, 5]).all())
     out[at // tile * tile:, g:, 5] = want[at // tile * tile:, g:, 5].float()
     ref.check(out, want, tol)
+
+
+@pytest.mark.parametrize("kernel,new", [(pa.PA_PREFILL_TWO_TILE, [3000, 1100]), (pa.PA_PREFILL_ONE_TILE, [1000, 96]),
+                                        (pa.PA_PREFILL_AUTO, [16, 40])])
+def test_prompts_repeat_bit_for_bit(kernel, new, plan):
+    """The score product of a chunk is issued behind the value product that reads the weights in the same
+    tensor memory, without a wait between them: any overtaking would show as other bits."""
+    lens = [4000, 1100]
+    c = ref.Cache(lens, 8, 128, 16, seed=17)
+    q = _q(sum(new), 32, 128, 18)
+    want, tol = ref.attention(c, q, new, 0.1)
+    start = _i32([0, new[0], sum(new)])
+    first = None
+    pa.pa_debug_set_prefill_kernel(kernel)
+    try:
+        for i in range(40):
+            out = torch.full(q.shape, math.nan, device="cuda")
+            pa.pa_prefill_q8(q, start, *c.args, c.dtables, c.dlens, 0.1, out, max(new), max(lens), plan)
+            if first is None:
+                first = out
+                ref.check(out, want, tol)
+            assert torch.equal(out, first), i
+    finally:
+        pa.pa_debug_set_prefill_kernel(pa.PA_PREFILL_AUTO)
