@@ -738,7 +738,8 @@ pa_status pa_prefill_window(const void* q, const int32_t* q_start, int num_queri
  * which the scores are finite in 32 bits, and any mix of v_scales from 2^-64 to
  * 2^120 (sequences whose blocks' span more than 2^80 may take up to twice the
  * time); a block with another scale (0, negative, out of range, NaN) makes the
- * rows that see it NaN. The codes may be copied like other bytes
+ * rows that see it NaN, and may so those of their tile (pa_prefill_q8) that do
+ * not. The codes may be copied like other bytes
  * (pa_copy_blocks over the pool as bf16 of half the D); a block's scales go
  * with it.
  *

@@ -548,9 +548,10 @@ __device__ __forceinline__ void q8_body(const CUtensorMap* kmap, const CUtensorM
         }
         ksl = ks * a.scale_log2;
         lvs = q8::log2_of(vs, ks);
-        // The value scales' range so far as a bit for every 2^6.17, behind the stages' bits: one
-        // reduction, and no register of its own (the kernels of two n-tiles have none left).
-        const uint32_t now = __reduce_or_sync(0xffffffffu, lane < ccnt ? 4u << ((__float2int_rd(lvs) + 64) * 83 >> 9) : 0u);
+        // The value scales' range so far as a bit for every 2^6.17 (from 2^-65: the logarithm is an
+        // approximation), behind the stages' bits: one reduction, and no register of its own (the
+        // kernels of two n-tiles have none left).
+        const uint32_t now = __reduce_or_sync(0xffffffffu, lane < ccnt ? 4u << ((__float2int_rd(lvs) + 65) * 83 >> 9) : 0u);
         badstage = (y.y ? badstage & 3u : badstage) | now;
     };
     make_batch();
