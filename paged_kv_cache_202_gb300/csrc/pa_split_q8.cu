@@ -31,7 +31,6 @@
 // The scales and table entries of up to 32 pages (a batch) are read by a lane each,
 // a batch ahead, and reach the tiles by shuffles.
 #include <algorithm>
-#include <type_traits>
 
 #include "pa_q8.cuh"
 #include "pa_split.cuh"
@@ -121,11 +120,11 @@ struct Q8State {
     }
 
     // The chunk's nv tokens, of rem before the sequence's end (MQ). Lane pg0 + j holds page j's scales: the keys' times the
-    // score scale and log2 e (ksl), and log2 of the values' (lvs). FAR: value scales far apart
+    // score scale and log2 e (ksl), and log2 of the values' (lvs). far: value scales far apart
     // (pa_q8.cuh).
-    template <int BS, bool FAR>
+    template <int BS>
     __device__ __forceinline__ void chunk(uint32_t kst, uint32_t vst, int nv, int lane, int pg0, float ksl, float lvs,
-                                          uint32_t qst, int nh, int rem, int nqb, int g) {
+                                          uint32_t qst, int nh, int rem, int nqb, int g, bool far) {
         if (nv < CT) {
             // Behind the end: whatever is there. No value of it may be NaN.
             for (int i = lane; i < (CT - nv) * (D / 16); i += 32)
@@ -223,8 +222,7 @@ struct Q8State {
                         x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
                         if (x > m[nt][j] + kRaise) {
                             const float f = fast_exp2(m[nt][j] - x);  // 0 at the segment's first tokens
-                            if constexpr (FAR) l[nt][j] = q8::times_exp2(l[nt][j], m[nt][j] - x);
-                            else l[nt][j] *= f;
+                            l[nt][j] = q8::times_exp2(l[nt][j], m[nt][j] - x);
                             m[nt][j] = x;
 #pragma unroll
                             for (int mt = 0; mt < KS; ++mt) {
@@ -245,16 +243,17 @@ struct Q8State {
                     float p[4];
 #pragma unroll
                     for (int i = 0; i < 4; ++i) p[i] = fast_exp2(s[t][nt][i] - base[i & 1]);
-                    if constexpr (FAR) {
-                        const float lv = __shfl_sync(0xffffffffu, lvs, pg0 + (sub + t * 16) / BS) - q8::kSumBias;
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) l[nt][i & 1] += fast_exp2(s[t][nt][i] - base[i & 1] - lv);
-                    } else {
-                        l[nt][0] = fmaf(p[0] + p[2], inv[t], l[nt][0]);
-                        l[nt][1] = fmaf(p[1] + p[3], inv[t], l[nt][1]);
-                    }
                     pb[t][nt][0] = movmatrix_trans(pack_f16x2(p[0], p[1]));
                     pb[t][nt][1] = movmatrix_trans(pack_f16x2(p[2], p[3]));
+                    float e = inv[t];
+                    if (far) {  // once more, without the value scale
+                        e = 1.f;
+                        const float lv = __shfl_sync(0xffffffffu, lvs, pg0 + (sub + t * 16) / BS) - q8::kSumBias;
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) p[i] = fast_exp2(s[t][nt][i] - base[i & 1] - lv);
+                    }
+                    l[nt][0] = fmaf(p[0] + p[2], e, l[nt][0]);
+                    l[nt][1] = fmaf(p[1] + p[3], e, l[nt][1]);
                 }
             }
             // Rows of the value tiles: token j, or j ^ 2, of the 16.
@@ -582,14 +581,10 @@ __device__ __forceinline__ void q8_body(const CUtensorMap* kmap, const CUtensorM
             poison = true;
         } else {
             const int rem = len[cb] - (cp + ci) * BS;
-            auto chunk = [&](auto far) {
-                st.template chunk<BS, decltype(far)::value>(stg, stg + kHalf, min(n * BS, rem), lane, ci, ksl, lvs,
-                                                            my_q, nh, rem, nqb, a.g);
-            };
             const uint32_t seen = badstage & ~3u;
             constexpr int kSteps = static_cast<int>(q8::kFarApart) * 83 / 512 - 1;  // so many lie within kFarApart
-            if (31 - __clz(seen) - (__ffs(seen) - 1) > kSteps) chunk(std::true_type());
-            else chunk(std::false_type());
+            st.template chunk<BS>(stg, stg + kHalf, min(n * BS, rem), lane, ci, ksl, lvs, my_q, nh, rem, nqb, a.g,
+                                  31 - __clz(seen) - (__ffs(seen) - 1) > kSteps);
         }
         ci += n;
         __syncwarp();
