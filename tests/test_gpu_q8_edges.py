@@ -203,3 +203,25 @@ def test_prompts_repeat_bit_for_bit(kernel, new, plan):
             assert torch.equal(out, first), i
     finally:
         pa.pa_debug_set_prefill_kernel(pa.PA_PREFILL_AUTO)
+
+
+@pytest.mark.parametrize("Hkv,D,bs", [(3, 64, 16), (2, 64, 32), (1, 128, 16)])
+def test_blocks_copied_with_their_scales(Hkv, D, bs, plan):
+    """Copy on write of a fork's blocks, as bf16 of half the width: the same codes, and the same rows."""
+    c = ref.Cache([200, 90], Hkv, D, bs, seed=19, slack=20)
+    used = c.tables[0, :-(-200 // bs)]
+    free = [x for x in range(c.NB) if x not in set(c.tables[c.tables >= 0].tolist())][:len(used)]
+    src, dst = _i32(used[:len(free)]), _i32(free)
+    before = [t.view(torch.uint8).clone() for t in c.args[:2]]
+    pa.pa_copy_blocks(*[p.view(torch.uint8).view(torch.bfloat16) for p in c.args[:2]], src, dst)
+    for s in c.args[2:]:
+        s[dst.long()] = s[src.long()]
+    for p, b in zip(c.args[:2], before):
+        want = b.clone()
+        want[dst.long()] = b[src.long()]
+        assert torch.equal(p.view(torch.uint8), want)
+    fork = c.dtables.clone()
+    fork[0, :len(free)] = dst
+    q = _q(2, 4 * Hkv, D, 20)
+    outs = [pa.pa_decode_q8(q, *c.args, t, c.dlens, 0.1, torch.zeros_like(q), 200, plan) for t in (c.dtables, fork)]
+    assert torch.equal(*outs)

@@ -131,6 +131,13 @@ def test_prefill_of_few_queries_takes_streams_past_32_bits(lib):
         assert _prefill(lib, B=8192, Hq=64, Hkv=64, mb=4095, maxlen=4095 * 16, mq=mq, T=40) == pa.PA_ERR_CUDA
 
 
+@pytest.mark.parametrize("D,dt,status", [(64, pa.PA_BF16, OK), (32, pa.PA_BF16, OK), (32, pa.PA_F32, SH),
+                                         (16, pa.PA_BF16, SH)])
+def test_block_copies_take_codes_as_bf16_of_half_the_width(lib, D, dt, status):
+    for bs in (16, 32):
+        assert lib.pa_copy_blocks(A, A, A, A, 0, 3, D, bs, 64, dt, None) == status
+
+
 def test_binding_refuses_host_tensors():
     z = torch.zeros
     i32 = torch.int32
