@@ -225,3 +225,19 @@ def test_blocks_copied_with_their_scales(Hkv, D, bs, plan):
     q = _q(2, 4 * Hkv, D, 20)
     outs = [pa.pa_decode_q8(q, *c.args, t, c.dlens, 0.1, torch.zeros_like(q), 200, plan) for t in (c.dtables, fork)]
     assert torch.equal(*outs)
+
+
+@pytest.mark.parametrize("scale", [-0.1, 0.0, -3.0])
+@pytest.mark.parametrize("Hq,Hkv,D", [(8, 2, 128), (17, 1, 64), (34, 2, 128)])
+def test_decode_of_any_score_scale(scale, Hq, Hkv, D, plan):
+    """Score scales that turn the order round, and none; heads that make slices of unequal size."""
+    lens = [700, 3, 33, 5000]
+    c = ref.Cache(lens, Hkv, D, 16, seed=21)
+    q = _q(4, Hq, D, 22)
+    # (The tolerance goes by the scale's magnitude.)
+    want, _ = ref.attention(c, q, [1] * 4, scale)
+    _, tol = ref.attention(c, -q if scale < 0 else q, [1] * 4, abs(scale))
+    out = torch.full((4, Hq, D), math.nan, device="cuda")
+    pa.pa_decode_q8(q, *c.args, c.dtables, c.dlens, scale, out, 5000, plan)
+    assert pa.pa_last_device_error(plan) == 0
+    ref.check(out, want, tol)
