@@ -20,8 +20,8 @@
 // to 2^-32 of the largest; l takes the weights unrounded.
 //
 // Measured (device time; a large bf16 product runs at 1945 TFLOP/s, 1733 sustained).
-// 16384 rows of one prompt, 32 / 8 heads: 1517 us, 1450 TFLOP/s (0.75, 0.84 of the
-// sustained rate). 16 sequences of 256 rows, 1024 to 16384 tokens: 259 us, 1243 TFLOP/s.
+// 16384 rows of one prompt, 32 / 8 heads: 1527 to 1550 us, 1430 TFLOP/s (0.73, 0.82 of the
+// sustained rate). 16 sequences of 256 rows, 1024 to 16384 tokens: 261 us, 1232 TFLOP/s.
 // Bound by a tile's chain: scores, softmax, weights, value product, about 3100 cycles for
 // a chunk of both tiles against 2200 of tensor work (59 % busy); issue slots are 57 %
 // full. What it does not spend its time on alone: without the exponentials 4.5 % less,

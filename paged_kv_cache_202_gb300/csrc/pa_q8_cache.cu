@@ -20,11 +20,13 @@
 // reads and turns them again, from L1, for the codes.
 //
 // Measured (device time; the copy rate is 6.8 TB/s). Write and read-back of 41084
-// prompt rows, 32 + 8 heads of 128 with norms: 227 us, 185 of them the write (0.90 GB
+// prompt rows, 32 + 8 heads of 128 with norms: 227 us, 187 of them the write (0.90 GB
 // of DRAM traffic, 4.9 TB/s): bound by issue slots (55 %, 2.3 instructions a clock) and
-// the latency of loads with 22 warps an SM. 64 rows: 9.6 us (6.4 and 3.5), two launches
-// and their chains of dependent lookups. Read-back of 89557 rows, 16 sequences: 85.6 us, 0.945 of
-// the copy rate. Slower for the 41084 rows: two blocks an SM with more rows in
+// the latency of loads with 22 warps an SM. 64 rows: 9.5 us (6.2 and 3.3), two launches
+// and their chains of dependent lookups. 3875 rows, 48 + 12 heads of 64, half rotated: 24.3 us,
+// 19.5 of them the write (57 MB, 2.9 TB/s: 139 blocks of the cache, in five parts each, are
+// 1.5 rounds of the blocks that fit the SMs). Read-back of 89557 rows, 16 sequences: 86 us, 0.94 of
+// the copy rate, in float32 142 us, 0.95, heads of 64 50 us, 0.81. Slower for the 41084 rows: two blocks an SM with more rows in
 // registers (234 to 249 us), weights folded into a table of the turns (238 to 250
 // us: the table's loads cost more than the products they save); asking for rows and
 // positions before the table entry arrives (64 rows 16.6 us, 12.0 without at the time);

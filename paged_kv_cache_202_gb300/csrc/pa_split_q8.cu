@@ -7,8 +7,8 @@
 // the values' scales sit in the exponents, so the value product takes the codes as
 // they are, and its weights, rounded to f16, keep 11 bits relative to the largest
 // for any mix of the scales that there are (pa_q8.cuh); l takes them unrounded. The
-// output in bf16 is as near to exact arithmetic as one of 32-bit weights (1.67e-3 against
-// 1.66e-3 of it). The reference m is raised only
+// output in bf16 is as near to exact arithmetic as one of 32-bit weights (1.67e-3 of its
+// norm against 1.66e-3; in float32 1.4e-4 to 2.0e-4). The reference m is raised only
 // when a score exceeds it by more than 8, so that most chunks need no maximum
 // across the warp (any reference gives the same quotient); weights are taken times
 // 2^7, so that f16 holds them up to there and down to 2^-32 of the largest. Codes become
@@ -606,14 +606,16 @@ __device__ __forceinline__ void q8_body(const CUtensorMap* kmap, const CUtensorM
 // allow: twelve, or eleven with two n-tiles.
 //
 // Measured (device time, split and merge; the copy rate is 6.8 TB/s). 64 sequences of
-// 512 to 32768 tokens, 32 / 8 heads of 128: 131.3 us for 0.80 GB, 6.10 TB/s (0.90), the
+// 512 to 32768 tokens, 32 / 8 heads of 128: 132 us for 0.80 GB, 6.05 TB/s (0.89), the
 // split kernel alone 124.8 us under the profiler with DRAM at 82 %; a kernel that only
 // reads as many 2 KB pages takes 122 us, this one from L2 95 us, so DRAM bounds it,
-// then the merge (7.4 us). 24 sequences of 8192 to 131072 tokens, 128 / 8 heads: 311 us
-// for 1.95 GB, 6.26 TB/s (0.92); with two n-tiles the tiles take 274 us from L2. 32 of
-// 128 to 2048, 32 / 32 heads: 35.8 us, 4.5 TB/s: 5 us of start, uneven ends, the merge.
-// One of 8191: 12.3 us: the chain of scan, table, scales and pages, and the merge.
-// 64 sequences, 4 newest queries each: 190 us.
+// then the merge (7.4 us). 24 sequences of 8192 to 131072 tokens, 128 / 8 heads: 311 to
+// 317 us for 1.95 GB, 6.2 TB/s (0.91); with two n-tiles the tiles take 274 us from L2. 32
+// of 128 to 2048, 32 / 32 heads: 36.6 us, 4.4 TB/s: 5 us of start, uneven ends, the merge.
+// One of 8191: 12.6 us: the chain of scan, table, scales and pages, and the merge.
+// 64 sequences, 4 newest queries each: 193 to 199 us. Heads of 64, whose pages are 1 KB:
+// 80 us for the first of these (0.73), 168 the second (0.85), 28.4 the third, 10.5 the
+// fourth.
 // Slower: one stage of 16 KB a warp (139 us for the first of these), smaller pieces
 // at the end of the page stream (their partials cost the merge more than they even out).
 template <int D, int BS, int NT, bool MQ>
