@@ -24,7 +24,7 @@
 // of DRAM traffic, 4.9 TB/s): bound by issue slots (55 %, 2.3 instructions a clock) and
 // the latency of loads with 22 warps an SM. 64 rows: 9.5 us (6.2 and 3.3), two launches
 // and their chains of dependent lookups. 3875 rows, 48 + 12 heads of 64, half rotated: 24.3 us,
-// 19.5 of them the write (57 MB, 2.9 TB/s: 139 blocks of the cache, in five parts each, are
+// 19.5 of them the write (65 MB, 3.4 TB/s: 139 blocks of the cache, in five parts each, are
 // 1.5 rounds of the blocks that fit the SMs). Read-back of 89557 rows, 16 sequences: 86 us, 0.94 of
 // the copy rate, in float32 142 us, 0.95, heads of 64 50 us, 0.81. Slower for the 41084 rows: two blocks an SM with more rows in
 // registers (234 to 249 us), weights folded into a table of the turns (238 to 250
